@@ -111,6 +111,18 @@ def lib():
         L.fp8_scaled_gemm_fp8out.restype = C.c_int
         L.fp8_scaled_gemm_fp8out.argtypes = [P, C.c_int, I64, Gran, P, P, C.c_int, I64, Gran, P, I64, I64,
                                              I64, P, C.c_int, C.c_int, P, P, P, I64, P, P, U32, P]
+        L.fp8_rmsnorm_quantize.restype = C.c_int
+        L.fp8_rmsnorm_quantize.argtypes = [P, C.c_int, I64, I64, I64, P, I64, P, C.c_int, F, Gran, C.c_int, C.c_int,
+                                           F, I32, P, P, P, I64, P, I64, P, P, P]
+        L.fp8_rmsnorm_backward.restype = C.c_int
+        L.fp8_rmsnorm_backward.argtypes = [P, C.c_int, I64, I64, I64, P, C.c_int, I64, P, C.c_int, P, P, I64, P,
+                                           I64, P, P]
+        L.fp8_kv_append.restype = C.c_int
+        L.fp8_kv_append.argtypes = [P, P, C.c_int, I64, I64, I64, I64, I64, P, P, I64, I64, P, I64, C.c_int, F, I32,
+                                    P, P, P, P, I64, I64, I64, I64, P]
+        L.fp8_paged_attention.restype = C.c_int
+        L.fp8_paged_attention.argtypes = [P, C.c_int, I64, I64, I64, I64, P, P, P, P, C.c_int, I64, I64, I64, I64, P,
+                                          I64, P, P, I64, I64, I64, F, I32, I64, P, C.c_int, I64, I64, P, P]
         _lib = L
     return _lib
 
@@ -384,7 +396,123 @@ def fp8_weight_only_gemm(x, w, fw, gw, scale_w, y, bias=None, flags=0, stream=No
                                       _stream(stream)))
 
 
-__all__ = ["fp8_pack_weights16", "fp8_quantize_packed16", "PackedWeights", "packed16_bytes", "B_PACKED16", "fp8_quant_error", "fp8_granularity_ledger", "LedgerSpec", "LedgerRow", "fp8_delayed_scale_update", "HIST_MAX", "HIST_LATEST", "fp8_weight_only_gemm", "fp8_scaled_gemm_fp8out", "fp8_amax", "fp8_compute_scale", "fp8_quantize", "fp8_quantize_transpose", "fp8_dequantize",
+def fp8_rmsnorm_quantize(x, weight, norm_eps, gran, fmt, mode, eps, pow2_round_up, scale, q, residual=None,
+                         h=None, rstd=None, inv_scale=None, amax_out=None, stream=None):
+    """Codes q and scales of RMSnorm(x + residual) * weight; h receives x + residual
+    (rounded to x's type), rstd [rows] the norm's factors for the gradient."""
+    rows, cols, ld = _mat(x)
+    qr, qc, ldq = _mat(q)
+    if (qr, qc) != (rows, cols) or q.dtype != torch.uint8:
+        raise ValueError("q must be uint8 [rows x cols]")
+    xt, ldr, ldh = _dtype(x), 0, 0
+    if residual is not None:
+        ldr = _like("residual", residual, rows, cols, x.dtype)
+    if h is not None:
+        ldh = _like("h", h, rows, cols, x.dtype)
+    _vec("weight", weight, cols)
+    if rstd is not None:
+        _vec("rstd", rstd, rows, torch.float32)
+    ns = ngroups(rows, gran[0]) * ngroups(cols, gran[1])
+    for name, t in (("scale", scale), ("inv_scale", inv_scale), ("amax_out", amax_out)):
+        if t is not None and (t.dtype != torch.float32 or t.numel() < ns or not t.is_contiguous()):
+            raise ValueError("%s must be contiguous float32 with one entry per group" % name)
+    _check("fp8_rmsnorm_quantize",
+           lib().fp8_rmsnorm_quantize(_ptr(x), xt, rows, cols, ld, _ptr(residual), ldr, _ptr(weight), _dtype(weight),
+                                      norm_eps, Gran(*gran), fmt, mode, eps, int(pow2_round_up), _ptr(scale),
+                                      _ptr(inv_scale), _ptr(q), ldq, _ptr(h), ldh, _ptr(rstd), _ptr(amax_out),
+                                      _stream(stream)))
+
+
+def fp8_rmsnorm_backward(dy, h, weight, rstd, dx, dweight=None, dresidual=None, stream=None):
+    """dx (the gradient of h = x + residual, dresidual added) and dweight of
+    fp8_rmsnorm_quantize, the cast taken as the identity."""
+    rows, cols, lddy = _mat(dy)
+    ldh = _like("h", h, rows, cols)
+    lddx = _like("dx", dx, rows, cols, dy.dtype)
+    lddr = _like("dresidual", dresidual, rows, cols, dy.dtype) if dresidual is not None else 0
+    _vec("weight", weight, cols)
+    _vec("rstd", rstd, rows, torch.float32)
+    if dweight is not None:
+        _vec("dweight", dweight, cols, torch.float32)
+    _check("fp8_rmsnorm_backward",
+           lib().fp8_rmsnorm_backward(_ptr(dy), _dtype(dy), rows, cols, lddy, _ptr(h), _dtype(h), ldh, _ptr(weight),
+                                      _dtype(weight), _ptr(rstd), _ptr(dresidual), lddr, _ptr(dx), lddx,
+                                      _ptr(dweight), _stream(stream)))
+
+
+def _like(name, t, rows, cols, dtype=None):
+    r, c, ld = _mat(t)
+    if (r, c) != (rows, cols) or (dtype is not None and t.dtype != dtype):
+        raise ValueError("%s must be [%d x %d]%s" % (name, rows, cols, "" if dtype is None else " %s" % dtype))
+    return ld
+
+
+def _vec(name, t, n, dtype=None):
+    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous() or (dtype is not None and t.dtype != dtype):
+        raise ValueError("%s must be a contiguous vector of %d%s" % (name, n, "" if dtype is None else " %s" % dtype))
+
+
+def _heads(name, t, heads=None, dim=None):
+    """(tokens, heads, dim, token stride, head stride) of [tokens x heads x dim] with unit last stride."""
+    if t.dim() != 3 or t.stride(2) != 1 or (heads, dim) not in ((None, None), t.shape[1:]):
+        raise ValueError("%s must be [tokens x heads x head_dim] with unit last stride%s" % (
+            name, "" if heads is None else ", %d heads of %d" % (heads, dim)))
+    return t.shape[0], t.shape[1], t.shape[2], t.stride(0), t.stride(1)
+
+
+def _paged(k_cache, v_cache, k_scale, v_scale, block_table, seq_start, kv_len):
+    """(pages, heads, page_size, head_dim, ld_table, seqs) of a paged cache and a batch's plan."""
+    shape = k_cache.shape
+    if (len(shape) != 4 or v_cache.shape != shape or k_cache.dtype != torch.uint8 or v_cache.dtype != torch.uint8
+            or not k_cache.is_contiguous() or not v_cache.is_contiguous()):
+        raise ValueError("k_cache and v_cache must be contiguous uint8 [pages x heads x page_size x head_dim]")
+    for t in (k_scale, v_scale):
+        if t.dtype != torch.float32 or t.shape != shape[:2] or not t.is_contiguous():
+            raise ValueError("k_scale and v_scale must be contiguous float32 [pages x heads]")
+    seqs = kv_len.shape[0]
+    if (block_table.dtype != torch.int32 or seq_start.dtype != torch.int32 or kv_len.dtype != torch.int32
+            or block_table.dim() != 2 or block_table.shape[0] != seqs or seq_start.shape != (seqs + 1,)
+            or block_table.stride(1) != 1 or not seq_start.is_contiguous() or not kv_len.is_contiguous()):
+        raise ValueError("block_table [seqs x n], seq_start [seqs + 1] and kv_len [seqs] must be int32 rows")
+    return (*shape, block_table.stride(0), seqs)
+
+
+def fp8_kv_append(k, v, k_cache, v_cache, k_scale, v_scale, fmt, block_table, seq_start, kv_len, max_new, eps=1e-12,
+                  pow2_round_up=False, stream=None):
+    """Quantizes new keys and values [tokens x heads x head_dim] into a paged cache of FP8 codes
+    [pages x heads x page_size x head_dim] with one scale per page and head."""
+    pages, heads, page, dim, ldt, seqs = _paged(k_cache, v_cache, k_scale, v_scale, block_table, seq_start, kv_len)
+    tokens, _, _, ldk, hdk = _heads("k", k, heads, dim)
+    tv, _, _, ldv, hdv = _heads("v", v, heads, dim)
+    if tv != tokens or v.dtype != k.dtype:
+        raise ValueError("k and v must have the same tokens and type")
+    _check("fp8_kv_append",
+           lib().fp8_kv_append(_ptr(k), _ptr(v), _dtype(k), tokens, ldk, hdk, ldv, hdv, _ptr(seq_start),
+                               _ptr(kv_len), seqs, max_new, _ptr(block_table), ldt, fmt, eps, int(pow2_round_up),
+                               _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), pages, heads, page, dim,
+                               _stream(stream)))
+
+
+def fp8_paged_attention(q, k_cache, v_cache, k_scale, v_scale, fmt, block_table, seq_start, kv_len, max_new, max_kv,
+                        sm_scale, y, causal=True, window=0, lse=None, stream=None):
+    """y = attention of the new tokens' queries q [tokens x q_heads x head_dim] (bf16) over the paged FP8
+    cache; max_new and max_kv bound the new tokens and the length of one sequence."""
+    pages, heads, page, dim, ldt, seqs = _paged(k_cache, v_cache, k_scale, v_scale, block_table, seq_start, kv_len)
+    tokens, qh, qd, ldq, hdq = _heads("q", q)
+    ty, yh, yd, ldy, hdy = _heads("y", y)
+    if qd != dim or (ty, yh, yd) != (tokens, qh, qd):
+        raise ValueError("q and y must be [tokens x q_heads x head_dim]")
+    if lse is not None and (lse.shape != (tokens, qh) or lse.dtype != torch.float32 or not lse.is_contiguous()):
+        raise ValueError("lse must be contiguous float32 [tokens x q_heads]")
+    _check("fp8_paged_attention",
+           lib().fp8_paged_attention(_ptr(q), _dtype(q), tokens, qh, ldq, hdq, _ptr(k_cache), _ptr(v_cache),
+                                     _ptr(k_scale), _ptr(v_scale), fmt, pages, heads, page, dim, _ptr(block_table),
+                                     ldt, _ptr(seq_start), _ptr(kv_len), seqs, max_new, max_kv, sm_scale,
+                                     int(causal), window, _ptr(y), _dtype(y), ldy, hdy, _ptr(lse), _stream(stream)))
+
+
+__all__ = ["fp8_rmsnorm_quantize", "fp8_rmsnorm_backward", "fp8_kv_append", "fp8_paged_attention",
+           "fp8_pack_weights16", "fp8_quantize_packed16", "PackedWeights", "packed16_bytes", "B_PACKED16", "fp8_quant_error", "fp8_granularity_ledger", "LedgerSpec", "LedgerRow", "fp8_delayed_scale_update", "HIST_MAX", "HIST_LATEST", "fp8_weight_only_gemm", "fp8_scaled_gemm_fp8out", "fp8_amax", "fp8_compute_scale", "fp8_quantize", "fp8_quantize_transpose", "fp8_dequantize",
            "fp8_amax_history_update", "fp8_scaled_gemm", "lib", "raw_call", "Gran", "Fp8rtError",
            "E4M3", "E5M2", "F32", "BF16", "DYNAMIC", "GIVEN", "POW2_SCALES", "EXACT_PRODUCTS", "EXACT_AUTO_BYTES", "FMAX", "ngroups",
            "scale_shape"]

@@ -531,4 +531,199 @@ fp8rt_status fp8_granularity_ledger(const void* w, fp8rt_dtype wt, int64_t N, in
   return FP8RT_OK;
 }
 
+fp8rt_status fp8_rmsnorm_quantize(const void* x, fp8rt_dtype xt, int64_t rows, int64_t cols, int64_t ldx,
+                                  const void* residual, int64_t ldr, const void* weight, fp8rt_dtype wt,
+                                  float norm_eps, fp8rt_gran g, fp8rt_format f, fp8rt_mode mode, float eps,
+                                  int32_t pow2_round_up, float* scale, float* inv_scale, uint8_t* q, int64_t ldq,
+                                  void* h_out, int64_t ldh, float* rstd_out, float* amax_out, hipStream_t stream) {
+  if (!valid_dtype(xt) || !valid_dtype(wt) || !valid_fmt(f) || !weight || !scale || !q) return FP8RT_EINVAL;
+  if (mode != FP8RT_DYNAMIC && mode != FP8RT_GIVEN) return FP8RT_EINVAL;
+  if (mode == FP8RT_DYNAMIC && !valid_eps(eps)) return FP8RT_EINVAL;
+  if (!isfinite(norm_eps) || norm_eps < 0.0f) return FP8RT_EINVAL;
+  fp8rt_status st = check_matrix(x, rows, cols, ldx, g);
+  if (st != FP8RT_OK) return st;
+  if (ldq < cols || (residual && ldr < cols) || (h_out && ldh < cols)) return FP8RT_EINVAL;
+  // in place or apart: a shifted view would be read after it is written
+  if (h_out && ((h_out == x && ldh != ldx) || (h_out == residual && ldh != ldr))) return FP8RT_EINVAL;
+  if (ldq % 16 != 0 || (residual && ldr % 16 != 0) || (h_out && ldh % 16 != 0)) return FP8RT_EALIGN;
+  if (!aligned16(q) || !aligned16(weight) || (residual && !aligned16(residual)) || (h_out && !aligned16(h_out)))
+    return FP8RT_EALIGN;
+  if (!aligned4(scale) || (inv_scale && !aligned4(inv_scale)) || (rstd_out && !aligned4(rstd_out)) ||
+      (amax_out && !aligned4(amax_out)))
+    return FP8RT_EALIGN;
+  if (cols > kNormMaxCols) return FP8RT_EUNSUPPORTED;
+  NormArgs a;
+  a.er = group_extent(rows, g.rows);
+  a.ec = group_extent(cols, g.cols);
+  if (a.er != 1) {
+    if (a.er != rows || a.ec != cols || mode != FP8RT_GIVEN) return FP8RT_EUNSUPPORTED;
+  } else if (a.ec != cols && ((a.ec & (a.ec - 1)) != 0 || a.ec > 512)) {
+    return FP8RT_EUNSUPPORTED;
+  }
+  a.x = x;
+  a.xt = xt;
+  a.rows = rows;
+  a.cols = cols;
+  a.ldx = ldx;
+  a.res = residual;
+  a.ldr = ldr;
+  a.w = weight;
+  a.wt = wt;
+  a.norm_eps = norm_eps;
+  a.fmt = f;
+  a.mode = mode;
+  a.eps = mode == FP8RT_DYNAMIC ? eps : 1.0f;
+  a.pow2 = pow2_round_up != 0;
+  a.scale = scale;
+  a.inv_scale = inv_scale;
+  a.q = q;
+  a.ldq = ldq;
+  a.h = h_out;
+  a.ldh = ldh;
+  a.rstd = rstd_out;
+  a.amax_out = amax_out;
+  return from_hip(launch_rmsnorm_quantize(a, stream));
+}
+
+fp8rt_status fp8_rmsnorm_backward(const void* dy, fp8rt_dtype dyt, int64_t rows, int64_t cols, int64_t lddy,
+                                  const void* h, fp8rt_dtype ht, int64_t ldh, const void* weight, fp8rt_dtype wt,
+                                  const float* rstd, const void* dresidual, int64_t lddr, void* dx, int64_t lddx,
+                                  float* dweight, hipStream_t stream) {
+  if (!valid_dtype(dyt) || !valid_dtype(ht) || !valid_dtype(wt) || !h || !weight || !rstd || !dx) return FP8RT_EINVAL;
+  fp8rt_status st = check_matrix(dy, rows, cols, lddy, fp8rt_gran{1, 0});
+  if (st != FP8RT_OK) return st;
+  if (ldh < cols || lddx < cols || (dresidual && lddr < cols)) return FP8RT_EINVAL;
+  if ((dx == dy && lddx != lddy) || (dx == dresidual && lddx != lddr) || dx == h) return FP8RT_EINVAL;
+  if (ldh % 16 != 0 || lddx % 16 != 0 || (dresidual && lddr % 16 != 0)) return FP8RT_EALIGN;
+  if (!aligned16(h) || !aligned16(weight) || !aligned16(dx) || (dresidual && !aligned16(dresidual)) ||
+      (dweight && !aligned16(dweight)) || !aligned4(rstd))
+    return FP8RT_EALIGN;
+  if (cols > kNormMaxCols) return FP8RT_EUNSUPPORTED;
+  NormGradArgs a;
+  a.dy = dy;
+  a.dyt = dyt;
+  a.rows = rows;
+  a.cols = cols;
+  a.lddy = lddy;
+  a.h = h;
+  a.ht = ht;
+  a.ldh = ldh;
+  a.w = weight;
+  a.wt = wt;
+  a.rstd = rstd;
+  a.dres = dresidual;
+  a.lddr = lddr;
+  a.dx = dx;
+  a.lddx = lddx;
+  a.dw = dweight;
+  return from_hip(launch_rmsnorm_backward(a, stream));
+}
+
+namespace {
+
+// The plan of a batch over a paged cache, shared by append and attention.
+fp8rt_status paged_setup(const int32_t* seq_start, const int32_t* kv_len, int64_t seqs, int64_t tokens,
+                         int64_t max_new, const int32_t* block_table, int64_t ld_table, int64_t pages, int64_t heads,
+                         int64_t page_size, int64_t head_dim, fp8rt_format f, PagedArgs& p) {
+  constexpr int64_t kMax = int64_t(1) << 31;
+  if (!seq_start || !kv_len || !block_table || !valid_fmt(f)) return FP8RT_EINVAL;
+  if (seqs <= 0 || tokens <= 0 || max_new <= 0 || ld_table <= 0 || pages <= 0 || heads <= 0 || page_size <= 0 ||
+      head_dim <= 0)
+    return FP8RT_EINVAL;
+  if (seqs >= kMax || tokens >= kMax || ld_table >= kMax || pages >= kMax || heads > 65535) return FP8RT_EINVAL;
+  if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) return FP8RT_EUNSUPPORTED;
+  if (head_dim != 64 && head_dim != 128) return FP8RT_EUNSUPPORTED;
+  // grids of 256 threads for every 16 new tokens of every sequence stay below 2^31 threads
+  if (seqs * (std::min(max_new, tokens) / 16 + 2) > (int64_t(1) << 23)) return FP8RT_EUNSUPPORTED;
+  if (!aligned4(seq_start) || !aligned4(kv_len) || !aligned4(block_table)) return FP8RT_EALIGN;
+  p.seq_start = seq_start;
+  p.kv_len = kv_len;
+  p.seqs = seqs;
+  p.tokens = tokens;
+  p.max_new = std::min(max_new, tokens);
+  p.table = block_table;
+  p.ld_table = ld_table;
+  p.pages = pages;
+  p.heads = static_cast<int>(heads);
+  p.page = static_cast<int>(page_size);
+  p.dim = static_cast<int>(head_dim);
+  p.fmt = f;
+  return FP8RT_OK;
+}
+
+}  // namespace
+
+fp8rt_status fp8_kv_append(const void* k, const void* v, fp8rt_dtype xt, int64_t tokens, int64_t ldk, int64_t hdk,
+                           int64_t ldv, int64_t hdv, const int32_t* seq_start, const int32_t* kv_len, int64_t seqs,
+                           int64_t max_new, const int32_t* block_table, int64_t ld_table, fp8rt_format f, float eps,
+                           int32_t pow2_round_up, uint8_t* k_cache, uint8_t* v_cache, float* k_scale,
+                           float* v_scale, int64_t pages, int64_t heads, int64_t page_size, int64_t head_dim,
+                           hipStream_t stream) {
+  if (!k || !v || !k_cache || !v_cache || !k_scale || !v_scale || !valid_dtype(xt) || !valid_eps(eps))
+    return FP8RT_EINVAL;
+  AppendArgs a;
+  const fp8rt_status st = paged_setup(seq_start, kv_len, seqs, tokens, max_new, block_table, ld_table, pages, heads,
+                                      page_size, head_dim, f, a.p);
+  if (st != FP8RT_OK) return st;
+  if (ldk < 0 || hdk < 0 || ldv < 0 || hdv < 0) return FP8RT_EINVAL;
+  if (ldk % 8 != 0 || hdk % 8 != 0 || ldv % 8 != 0 || hdv % 8 != 0) return FP8RT_EALIGN;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned4(k_scale) ||
+      !aligned4(v_scale))
+    return FP8RT_EALIGN;
+  a.k = k;
+  a.v = v;
+  a.xt = xt;
+  a.ldk = ldk;
+  a.hdk = hdk;
+  a.ldv = ldv;
+  a.hdv = hdv;
+  a.eps = eps;
+  a.pow2 = pow2_round_up != 0;
+  a.kc = k_cache;
+  a.vc = v_cache;
+  a.ks = k_scale;
+  a.vs = v_scale;
+  return from_hip(launch_kv_append(a, stream));
+}
+
+fp8rt_status fp8_paged_attention(const void* q, fp8rt_dtype qt, int64_t tokens, int64_t q_heads, int64_t ldq,
+                                 int64_t hdq, const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale,
+                                 const float* v_scale, fp8rt_format f, int64_t pages, int64_t heads,
+                                 int64_t page_size, int64_t head_dim, const int32_t* block_table, int64_t ld_table,
+                                 const int32_t* seq_start, const int32_t* kv_len, int64_t seqs, int64_t max_new,
+                                 int64_t max_kv, float sm_scale, int32_t causal, int64_t window, void* y,
+                                 fp8rt_dtype yt, int64_t ldy, int64_t hdy, float* lse, hipStream_t stream) {
+  if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !y || !valid_dtype(qt) || !valid_dtype(yt))
+    return FP8RT_EINVAL;
+  AttendArgs a;
+  const fp8rt_status st = paged_setup(seq_start, kv_len, seqs, tokens, max_new, block_table, ld_table, pages, heads,
+                                      page_size, head_dim, f, a.p);
+  if (st != FP8RT_OK) return st;
+  if (q_heads <= 0 || q_heads > 65535 || q_heads % heads != 0 || max_kv <= 0 || window < 0 || !isfinite(sm_scale))
+    return FP8RT_EINVAL;
+  if (ldq < 0 || hdq < 0 || ldy < 0 || hdy < 0) return FP8RT_EINVAL;
+  if (qt != FP8RT_BF16 || yt != FP8RT_BF16) return FP8RT_EUNSUPPORTED;  // activations stay BF16
+  if (ldq % 8 != 0 || hdq % 8 != 0 || ldy % 4 != 0 || hdy % 4 != 0) return FP8RT_EALIGN;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned4(k_scale) || !aligned4(v_scale) ||
+      (reinterpret_cast<uintptr_t>(y) & 7u) || (lse && !aligned4(lse)))
+    return FP8RT_EALIGN;
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_heads = q_heads;
+  a.ldq = ldq;
+  a.hdq = hdq;
+  a.kc = k_cache;
+  a.vc = v_cache;
+  a.ks = k_scale;
+  a.vs = v_scale;
+  a.max_kv = std::min(max_kv, ld_table * page_size);
+  a.sm_scale = sm_scale;
+  a.causal = causal != 0;
+  a.window = window;
+  a.y = static_cast<uint16_t*>(y);
+  a.ldy = ldy;
+  a.hdy = hdy;
+  a.lse = lse;
+  return from_hip(launch_paged_attention(a, stream));
+}
+
 }  // extern "C"

@@ -210,4 +210,94 @@ hipError_t launch_gemm_skinny(const GemmArgs& g, hipStream_t stream);
 hipError_t launch_pack_weights16(const uint8_t* q, int64_t N, int64_t K, int64_t ldq, uint8_t* qp,
                                  hipStream_t stream);
 
+// RMS norm with residual and FP8 output, and its gradient (norm.hip).
+struct NormArgs {
+  const void* x = nullptr;  // type xt
+  int xt = 0;
+  int64_t rows = 0, cols = 0, ldx = 0;
+  const void* res = nullptr;  // type xt, nullable
+  int64_t ldr = 0;
+  const void* w = nullptr;
+  int wt = 0;
+  float norm_eps = 0.0f;
+  int64_t er = 1, ec = 0;  // effective group extents: er 1 (rows, groups) or rows (tensor)
+  int fmt = 0, mode = 0;
+  float eps = 1.0f;
+  int pow2 = 0;
+  float* scale = nullptr;
+  float* inv_scale = nullptr;
+  uint8_t* q = nullptr;
+  int64_t ldq = 0;
+  void* h = nullptr;  // nullable
+  int64_t ldh = 0;
+  float* rstd = nullptr;
+  float* amax_out = nullptr;
+};
+hipError_t launch_rmsnorm_quantize(const NormArgs& a, hipStream_t stream);
+
+struct NormGradArgs {
+  const void* dy = nullptr;
+  int dyt = 0;
+  int64_t rows = 0, cols = 0, lddy = 0;
+  const void* h = nullptr;
+  int ht = 0;
+  int64_t ldh = 0;
+  const void* w = nullptr;
+  int wt = 0;
+  const float* rstd = nullptr;
+  const void* dres = nullptr;
+  int64_t lddr = 0;
+  void* dx = nullptr;
+  int64_t lddx = 0;
+  float* dw = nullptr;
+};
+constexpr int64_t kNormMaxCols = 32768;  // 1024 threads hold a row, 32 elements each
+hipError_t launch_rmsnorm_backward(const NormGradArgs& a, hipStream_t stream);
+
+// The paged FP8 cache of keys and values (kv_append.hip, paged_attention.hip).
+// Device-side integers are not trusted: every kernel clamps them (SeqSpan).
+struct PagedArgs {
+  const int32_t* seq_start = nullptr;
+  const int32_t* kv_len = nullptr;
+  int64_t seqs = 0, tokens = 0, max_new = 0;
+  const int32_t* table = nullptr;
+  int64_t ld_table = 0;
+  int64_t pages = 0;
+  int heads = 0, page = 0, dim = 0;
+  int fmt = 0;
+};
+
+struct AppendArgs {
+  PagedArgs p;
+  const void* k = nullptr;
+  const void* v = nullptr;
+  int xt = 0;
+  int64_t ldk = 0, hdk = 0, ldv = 0, hdv = 0;
+  float eps = 1.0f;
+  int pow2 = 0;
+  uint8_t* kc = nullptr;
+  uint8_t* vc = nullptr;
+  float* ks = nullptr;
+  float* vs = nullptr;
+};
+hipError_t launch_kv_append(const AppendArgs& a, hipStream_t stream);
+
+struct AttendArgs {
+  PagedArgs p;
+  const uint16_t* q = nullptr;  // bf16
+  int64_t q_heads = 0, ldq = 0, hdq = 0;
+  const uint8_t* kc = nullptr;
+  const uint8_t* vc = nullptr;
+  const float* ks = nullptr;
+  const float* vs = nullptr;
+  int64_t max_kv = 0;
+  float sm_scale = 1.0f;
+  int causal = 0;
+  int64_t window = 0;
+  uint16_t* y = nullptr;  // bf16
+  int64_t ldy = 0, hdy = 0;
+  float* lse = nullptr;
+};
+hipError_t launch_paged_attention(const AttendArgs& a, hipStream_t stream);
+
 }  // namespace fp8rt

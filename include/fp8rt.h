@@ -440,6 +440,126 @@ fp8rt_status fp8_granularity_ledger(const void* w, fp8rt_dtype wt, int64_t N, in
                                     const fp8rt_ledger_spec* specs, int32_t n_specs,
                                     fp8rt_ledger_row* rows, hipStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Operators of a decoder layer between the scaled GEMMs.  These are this
+ * library's own additions to the chain, defined by the formulas below; their
+ * scales, casts and non-finite rules are those of fp8_quantize. */
+
+/* Root-mean-square norm with the residual's addition and an FP8 output: the
+ * operand of the next scaled GEMM in one pass over its input.
+ *   h[i,j] = x[i,j] + residual[i,j]            (binary32; x alone without residual)
+ *   rstd_i = 1 / sqrt(mean_j h[i,j]^2 + norm_eps)
+ *   y[i,j] = h[i,j] * weight[j] * rstd_i       (binary32)
+ *   q, scale, inv_scale = fp8_quantize(y, g, f, mode, eps, pow2_round_up)
+ *   x, residual (nullable) : [rows x cols] fp32 / bf16 (xt), leading dimensions
+ *              ldx, ldr;  weight : [cols] fp32 / bf16 (wt)
+ *   h_out    : nullable [rows x cols] of type xt (ldh): h rounded once; the norm
+ *              is taken of the unrounded sum.  h_out may be x or residual itself
+ *              (same pointer and leading dimension), not overlap them otherwise
+ *   rstd_out : nullable [rows] fp32, for fp8_rmsnorm_backward
+ *   amax_out : nullable, the observed max |y| of each group (for delayed scaling)
+ * Granularities: rows {1,0}; groups {1,g}, g = 16, 32, 64, 128, 256 or 512; the whole
+ * tensor {0,0} with FP8RT_GIVEN only (a delayed scale: the cast cannot wait
+ * for an amax of all rows), else FP8RT_EUNSUPPORTED.  GIVEN reads scale (and
+ * inv_scale if not NULL, else r = fl32(1/s)).
+ * norm_eps: finite, >= 0.  Alignment as fp8_quantize: cols and leading
+ * dimensions multiples of 16, pointers of matrices and weight 16-byte aligned.
+ * cols <= 32768 (a row stays in registers), else FP8RT_EUNSUPPORTED.  Workspace: the per-stream workspace holds the amax partials
+ * of the {0,0} case. */
+fp8rt_status fp8_rmsnorm_quantize(const void* x, fp8rt_dtype xt, int64_t rows, int64_t cols, int64_t ldx,
+                                  const void* residual, int64_t ldr, const void* weight, fp8rt_dtype wt,
+                                  float norm_eps, fp8rt_gran g, fp8rt_format f, fp8rt_mode mode, float eps,
+                                  int32_t pow2_round_up, float* scale, float* inv_scale, uint8_t* q, int64_t ldq,
+                                  void* h_out, int64_t ldh, float* rstd_out, float* amax_out, hipStream_t stream);
+
+/* Gradient of that norm (the cast counts as the identity: a straight-through
+ * estimator, as FP8 training recipes take it).  With n = h rstd, gy = dy weight:
+ *   dx[i,j]    = rstd_i (gy[i,j] - n[i,j] mean_k(gy[i,k] n[i,k])) + dresidual[i,j]
+ *   dweight[j] = sum_i dy[i,j] n[i,j]
+ * dx is the gradient of h, that is of x and of residual alike; dresidual
+ * (nullable) is the gradient that reaches h along the residual path.
+ *   dy, dresidual, dx : [rows x cols] of type dyt;  h : [rows x cols] of type ht
+ *   (h_out of the forward, or x when there was no residual);  weight : [cols] (wt)
+ *   rstd : [rows] fp32 (rstd_out);  dweight : nullable [cols] fp32, OVERWRITTEN
+ * dx may be dy or dresidual itself (same pointer and leading dimension).  Sums are
+ * binary32 in a fixed order: the results do not change from run to run.
+ * Alignment: cols and leading dimensions multiples of 16, matrices, weight and
+ * dweight 16-byte aligned, cols <= 32768 (else FP8RT_EUNSUPPORTED).
+ * Scratch: the per-stream scratch buffer holds the dweight partials (at most
+ * 512 x cols floats). */
+fp8rt_status fp8_rmsnorm_backward(const void* dy, fp8rt_dtype dyt, int64_t rows, int64_t cols, int64_t lddy,
+                                  const void* h, fp8rt_dtype ht, int64_t ldh, const void* weight, fp8rt_dtype wt,
+                                  const float* rstd, const void* dresidual, int64_t lddr, void* dx, int64_t lddx,
+                                  float* dweight, hipStream_t stream);
+
+/* A paged key / value cache of FP8 codes, one fp32 scale for each page and head:
+ *   k_cache, v_cache : [pages][heads][page_size][head_dim] codes (contiguous)
+ *   k_scale, v_scale : [pages][heads] fp32, the dequantization scale
+ * page_size 16, 32, 64 or 128 tokens; head_dim 64 or 128; seqs * (max_new / 16 +
+ * 2) <= 2^23 (else FP8RT_EUNSUPPORTED).  Position p of
+ * sequence b lives in slot p % page_size of page block_table[b][p / page_size]
+ * (int32, leading dimension ld_table >= 1 entries).
+ * A batch of `seqs` sequences hands in `tokens` new tokens, packed:
+ *   seq_start : int32 [seqs + 1], sequence b owns tokens seq_start[b] ..
+ *               seq_start[b+1] - 1 (none is allowed)
+ *   kv_len    : int32 [seqs], the sequence's length INCLUDING its new tokens, so
+ *               the new ones are its last seq_start[b+1] - seq_start[b] positions
+ *   max_new   : a bound on the new tokens of one sequence (host)
+ * These arrays live on the device and are not read by the host: the kernels
+ * bound every index by tokens, pages, ld_table and max_new.  A table entry outside
+ * [0, pages) stands for a page that is not there (nothing is written to it,
+ * attention takes its positions as hidden); positions past ld_table *
+ * page_size and before 0 are dropped in the same way, and so are tokens past max_new.
+ *
+ * fp8_kv_append writes the new tokens' keys and values into the cache.  For
+ * each page and head that receives tokens, a = max |x| over what it receives:
+ *   a page that held no token of the sequence before: s, r from a as fp8_quantize
+ *   a page partly filled by earlier tokens (scale s0): s, r from a if that s >= s0,
+ *     else s = s0, r = fl32(1/s0); when s grows past s0, the earlier tokens' codes become
+ *     RNE(clamp(dec(code) * fl32(s0 / s))) (exact up to underflow with pow2_round_up)
+ *   codes of the new tokens RNE(clamp(fl32(x r))), NaN -> 0x7F.
+ * A NaN or Inf makes its page's scale NaN for that head.  Two sequences must not
+ * share a page that receives tokens in the call.  Calling again with the same
+ * arguments changes nothing.
+ *   k, v : token t, head h, element d at [t * ldk + h * hdk + d] (ldv, hdv for v), fp32 / bf16 (xt)
+ * Alignment: ldk, hdk, ldv, hdv multiples of 8, k, v, k_cache, v_cache 16-byte
+ * aligned. */
+fp8rt_status fp8_kv_append(const void* k, const void* v, fp8rt_dtype xt, int64_t tokens, int64_t ldk, int64_t hdk,
+                           int64_t ldv, int64_t hdv, const int32_t* seq_start, const int32_t* kv_len, int64_t seqs,
+                           int64_t max_new, const int32_t* block_table, int64_t ld_table, fp8rt_format f, float eps,
+                           int32_t pow2_round_up, uint8_t* k_cache, uint8_t* v_cache, float* k_scale,
+                           float* v_scale, int64_t pages, int64_t heads, int64_t page_size, int64_t head_dim,
+                           hipStream_t stream);
+
+/* Attention of the new tokens over that cache (their own keys and values
+ * appended before): single tokens, chunks of prompts and whole prompts alike.
+ * Query t of sequence b stands at position p = kv_len[b] - seq_start[b+1] + t;
+ * query head h reads key / value head h / (q_heads / heads).
+ *   z[j]  = sm_scale * sum_d q[t,h,d] k[j,d],     k[j,d] = k_scale dec(code)
+ *   y     = sum_j e^(z[j] - m) v[j] / sum_j e^(z[j] - m),  m = max_j z[j]
+ * over the visible positions j: 0 <= j < kv_len[b]; j <= p if causal; j > p - window if
+ * window > 0; j's page present.  Hidden positions count for nothing whatever they hold (NaN
+ * codes or scales, stale or missing pages).  A query that sees no position gives y = 0 and lse = -Inf.
+ * Keys and queries are multiplied as bf16 (every FP8 value is one) and
+ * accumulated in FP32; softmax statistics are FP32; the weights e^(z - m) are
+ * rounded to fp16 (11 bits, times the page's v scale relative to the largest seen) for the
+ * second product, whose accumulation is FP32.
+ *   q : bf16, token t, head h, element d at [t * ldq + h * hdq + d] (qt must be FP8RT_BF16)
+ *   y : bf16, at [t * ldy + h * hdy + d] (yt must be FP8RT_BF16);
+ *   lse : nullable fp32 [tokens][q_heads]: m + ln(sum_j e^(z[j] - m))
+ *   max_kv : a bound on kv_len (host), used to choose how the work is split; longer
+ *            sequences are still computed
+ * q_heads a multiple of heads; sm_scale finite; window >= 0.
+ * Alignment: ldq, hdq multiples of 8, ldy, hdy of 4, q and the caches 16-byte, y 8-byte aligned.
+ * Scratch: the per-stream scratch buffer holds the parts of sequences split along their keys. */
+fp8rt_status fp8_paged_attention(const void* q, fp8rt_dtype qt, int64_t tokens, int64_t q_heads, int64_t ldq,
+                                 int64_t hdq, const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale,
+                                 const float* v_scale, fp8rt_format f, int64_t pages, int64_t heads,
+                                 int64_t page_size, int64_t head_dim, const int32_t* block_table, int64_t ld_table,
+                                 const int32_t* seq_start, const int32_t* kv_len, int64_t seqs, int64_t max_new,
+                                 int64_t max_kv, float sm_scale, int32_t causal, int64_t window, void* y,
+                                 fp8rt_dtype yt, int64_t ldy, int64_t hdy, float* lse, hipStream_t stream);
+
 /* Human-readable name of a status code (static storage). */
 const char* fp8rt_status_string(fp8rt_status s);
 
