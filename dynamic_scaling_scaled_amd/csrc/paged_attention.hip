@@ -1,98 +1,777 @@
 // paged_attention.hip -- attention over a paged cache of FP8 codes with one
 // scale for each page and head.
 //
-// One wave per query and head: each lane scores one of 64 positions, the
-// softmax's running maximum and sum are joined over the wave, and each lane
-// then adds its share of the head's dimensions for all 64.
+// Mathematics.  With t_j = z_j log2(e) the scores of the visible positions and
+// v_j = s_j dec(code_j) their values (s_j the page's v scale), the weight
+//   w_j = 2^(t_j + log2 s_j - m),   m >= max_j (t_j + log2 s_j) - kSlack,
+// turns the output into  y = sum_j w_j dec(code_j) / sum_j (w_j / s_j):  the codes go
+// into the second matrix product as they are, the weights reach at most
+// 2^kSlack whatever the pages' scales, and the sums follow in one pass over the keys
+// (when m moves, the sums so far are multiplied by 2^(m_old - m_new)).
+// m + log2 sum_j (w_j / s_j) is the log-sum-exp in base 2.
+//
+// Roundings.  Every FP8 code is a bf16 and an fp16 value, so q k multiplies exact
+// operands (bf16 MFMA) and the codes enter the second product exactly (fp16 MFMA); the weights are
+// rounded to fp16 (11 bits; bf16's 8 bits would add as much error as the bf16
+// output itself has); sums, maxima and accumulators are binary32.
+//
+// Orientation.  The scores are computed transposed, S^T = K Q^T: a lane then holds
+// one query row's scores for several keys, which is the operand layout that the
+// second product Y^T = V^T P^T wants, with the keys of a matrix instruction in the order in which
+// the lane has them.  No score crosses lanes; a row's maximum and sum do only when they must.
+//
+// A query row is a (token, head of the group) pair: row r of a sequence and
+// key / value head is token r / group, head r % group, so the heads that share keys share
+// their loads.  Two kernels: k_attend_few for up to 16 rows (decode), each wave streaming its own
+// keys from HBM; k_attend_many, 128 rows a workgroup, keys and values staged in LDS.
+// Long key ranges are cut into chunks, whose unnormalised sums k_attend_join adds.
+#include <algorithm>
+#include <type_traits>
+
 #include "paged_common.h"
 
 namespace fp8rt {
 
 namespace {
 
-template <int F, int D>
-__global__ void __launch_bounds__(64) k_attend(AttendArgs a, int64_t grid_n) {
-  constexpr int E = D / 64;  // dimensions of one lane
-  __shared__ float qs[D];
-  const int lane = threadIdx.x;
-  const int64_t b = blockIdx.x / grid_n;
-  const int64_t i = blockIdx.x % grid_n;
-  const int64_t h = blockIdx.y;
-  const SeqSpan s = seq_span(a.p, b);
-  if (i >= s.n) return;
-  const int64_t tok = s.tok0 + i, at = s.first + i;
-  const int head = static_cast<int>(h / (a.q_heads / a.p.heads));
-  const int page = a.p.page;
-  for (int e = 0; e < E; ++e) {
-    const int d = lane * E + e;
-    qs[d] = __uint_as_float(static_cast<uint32_t>(a.q[tok * a.ldq + h * a.hdq + d]) << 16);
-  }
-  __syncthreads();
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+// The running maximum follows only when a row passes it by 2^8: weights stay
+// below fp16's largest value, and the sums are seldom rescaled.
+constexpr float kSlack = 8.0f;
+// Scales below the smallest normal count as that: log2 and 1 / s stay finite.
+constexpr float kTinyScale = 0x1p-126f;
+
+// Two codes (a half of a dword) as two bf16 / fp16 values, exactly.
+template <int F, bool HI>
+__device__ __forceinline__ uint32_t to_bf16(uint32_t w) {
+  if constexpr (F == kE4M3)
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI));
+  else
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, 1.0f, HI));
+}
+template <int F, bool HI>
+__device__ __forceinline__ uint32_t to_f16(uint32_t w) {
+  if constexpr (F == kE4M3)
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, HI));
+  else
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_bf8(w, 1.0f, HI));
+}
+template <int F>
+__device__ __forceinline__ u32x4 bf16_of(uint32_t a, uint32_t b) {
+  return u32x4{to_bf16<F, false>(a), to_bf16<F, true>(a), to_bf16<F, false>(b), to_bf16<F, true>(b)};
+}
+template <int F>
+__device__ __forceinline__ u32x4 f16_of(uint32_t a, uint32_t b) {
+  return u32x4{to_f16<F, false>(a), to_f16<F, true>(a), to_f16<F, false>(b), to_f16<F, true>(b)};
+}
+
+// Whether any of four codes is a NaN or an infinity: the magnitude bits reach
+// 0x7F (E4M3) or 0x7C (E5M2), so adding the rest to 0x80 carries into a byte's top bit.
+template <int F>
+__device__ __forceinline__ uint32_t non_finite(uint32_t w) {
+  return ((w & 0x7F7F7F7Fu) + (F == kE4M3 ? 0x01010101u : 0x04040404u)) & 0x80808080u;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), f16x2));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  bf16x2 v;
+  v[0] = static_cast<__bf16>(a);
+  v[1] = static_cast<__bf16>(b);
+  return __builtin_bit_cast(uint32_t, v);
+}
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float log2_fast(float x) { return __builtin_amdgcn_logf(x); }
+
+// Visible positions of one query: [lo, hi).
+struct Range {
+  int32_t lo, hi;
+};
+
+__device__ __forceinline__ Range visible(const AttendArgs& a, const SeqSpan& s, int64_t token) {
+  const int64_t at = s.first + token;
   int64_t lo = 0, hi = s.len;
   if (a.causal && at + 1 < hi) hi = at + 1;
   if (a.window > 0 && at - a.window + 1 > 0) lo = at - a.window + 1;
-  float m = -INFINITY, l = 0.0f, y[E] = {};
-  for (int64_t j0 = lo / 16 * 16; j0 < hi; j0 += 64) {
-    const int64_t j = j0 + lane;
-    const bool inside = j >= lo && j < hi;
-    const int32_t pg = inside ? page_of(a.p, b, j / page) : -1;
-    const bool seen = pg >= 0;
-    float z = -INFINITY, vs = 0.0f;
-    if (seen) {
-      const uint32_t* k = reinterpret_cast<const uint32_t*>(
-          a.kc + ((int64_t(pg) * a.p.heads + head) * page + j % page) * D);
-      float dot = 0.0f;
-      for (int d = 0; d < D; d += 4) {
-        float v[4];
-        decode4<F>(k[d / 4], v);
-        for (int t = 0; t < 4; ++t) dot += v[t] * qs[d + t];
-      }
-      z = dot * a.ks[int64_t(pg) * a.p.heads + head] * a.sm_scale;
-      vs = a.vs[int64_t(pg) * a.p.heads + head];
+  if (hi < 0) hi = 0;
+  if (lo > hi) lo = hi;
+  return Range{static_cast<int32_t>(lo), static_cast<int32_t>(hi)};
+}
+
+// What a tile of `rows` query rows from row r0 sees together (its first row
+// starts first, its last row ends last), from a multiple of 64 on.
+__device__ __forceinline__ Range tile_range(const AttendArgs& a, const SeqSpan& s, int32_t r0, int32_t rows,
+                                            int32_t group) {
+  const int64_t last = (int64_t(r0) + rows - 1) / group;
+  const Range x = visible(a, s, r0 / group), y = visible(a, s, last < s.n ? last : s.n - 1);
+  return Range{x.lo / 64 * 64, y.hi};
+}
+
+// How the keys of a tile are cut: `chunks` pieces of `len` keys (a multiple
+// of 64), the last one open-ended.
+struct Cut {
+  int32_t chunks, len;
+};
+
+__device__ __forceinline__ Range chunk_of(const Range& t, const Cut& c, int32_t i) {
+  const int64_t lo = int64_t(t.lo) + int64_t(i) * c.len, hi = lo + c.len;
+  return Range{lo < t.hi ? static_cast<int32_t>(lo) : t.hi,
+               i == c.chunks - 1 || hi > t.hi ? t.hi : static_cast<int32_t>(hi)};
+}
+
+// Partial results of cut tiles, in the stream's scratch.
+struct Parts {
+  float* o;    // [chunk][token][q head][D], unnormalised
+  float2* ml;  // [chunk][token][q head]: m, sum of w / s
+};
+
+// What one 16-key part of a step needs from its page: t = dot * c, log2 of the v scale, its inverse.
+// A v scale that is not finite counts as 1 here (scores and sums do not depend on
+// it); its values are put right by blown_up on the way that takes such steps.
+constexpr int kAbsent = 0, kFine = 1, kNaNScale = 2, kInfScale = 3;
+struct PartScale {
+  float c, lv, inv;
+  int kind;
+};
+__device__ __forceinline__ PartScale part_scale(int32_t pg, float ks, float vs, float sm) {
+  const bool nan = __builtin_isnan(vs), inf = vs > 3.4028235e38f;
+  const float v = nan || inf ? 1.0f : vs < kTinyScale ? kTinyScale : vs;
+  return PartScale{ks * sm, log2_fast(v), 1.0f / v, pg < 0 ? kAbsent : nan ? kNaNScale : inf ? kInfScale : kFine};
+}
+
+// Two fp16 code values under a scale that is NaN or infinite: NaN, or an
+// infinity of the code's sign (0 * Inf is NaN).
+__device__ __forceinline__ uint32_t blown_up(uint32_t x, int kind) {
+  uint32_t r = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t v = x >> (16 * i) & 0xFFFFu, mag = v & 0x7FFFu;
+    const uint32_t y = kind == kNaNScale || mag == 0 || mag > 0x7C00u ? 0x7E00u : (v & 0x8000u) | 0x7C00u;
+    r |= y << (16 * i);
+  }
+  return r;
+}
+
+// ---------------------------------------------------------------------------
+// Up to 16 query rows: decode.  A workgroup takes one tile of 16 rows and one
+// chunk of keys; its waves take 32-key steps in turn, each with its own
+// running maximum and sums, joined through LDS at the end.  The keys of a
+// step go from HBM to registers in operand order: lane l (c = l % 16, g = l / 16)
+// loads 16-byte pieces of key c of each 16-key part, and for the keys
+// {4g..4g+3, 16+4g..16+4g+3}, whose scores it will hold, D/16 bytes of the values.
+template <int F, int D, int W>
+__global__ void __launch_bounds__(64 * W, W == 4 ? 3 : 1)
+    k_attend_few(AttendArgs a, Cut cut, int32_t tiles, Parts parts) {
+  constexpr int KD = D / 64;      // 16-byte key pieces of a lane and part
+  constexpr int VW = D / 64;      // dwords of a lane and key
+  constexpr int DT = D / 16;      // 16-wide output tiles: tile 4w + b is byte b of dword w
+  constexpr int LD = D + 4;
+  __shared__ __align__(16) float sh_o[W][16][LD];
+  __shared__ float2 sh_ml[W][16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = lane & 15, g = lane >> 4;
+  const int32_t heads = a.p.heads, group = static_cast<int32_t>(a.q_heads / heads);
+  int64_t blk = blockIdx.x;
+  const int32_t head = static_cast<int32_t>(blk % heads);
+  blk /= heads;
+  const int32_t chunk = static_cast<int32_t>(blk % cut.chunks);
+  blk /= cut.chunks;
+  const int32_t r0 = static_cast<int32_t>(blk % tiles) * 16;
+  const int64_t b = blk / tiles;
+  const SeqSpan s = seq_span(a.p, b);
+  const int64_t all = int64_t(s.n) * group;
+  if (r0 >= all) return;
+  const int32_t rows = all - r0 < 16 ? static_cast<int32_t>(all - r0) : 16;
+  const Range tile = tile_range(a, s, r0, rows, group);
+  const Range part = chunk_of(tile, cut, chunk);
+  if (chunk > 0 && part.lo >= part.hi) return;  // (chunk 0 also writes the rows that see nothing)
+  const int32_t page = a.p.page;
+  // this lane's query row
+  const int32_t r = r0 + (c < rows ? c : 0);
+  const int64_t tok = s.tok0 + r / group;
+  const int64_t qh = int64_t(head) * group + r % group;
+  Range see = visible(a, s, r / group);
+  if (c >= rows) see.hi = see.lo;
+  // positions that every row sees, and that any row sees
+  const Range first = visible(a, s, r0 / group), last = visible(a, s, (r0 + rows - 1) / group);
+  const int32_t all_lo = last.lo, all_hi = first.hi, any_lo = first.lo;
+  const float sm = fabsf(a.sm_scale) * kLog2e;
+  const uint32_t flip = a.sm_scale < 0.0f ? 0x80008000u : 0u;  // a negative scale negates the query
+  // q in key order: piece h, half u of a 16-byte piece -> dimensions 64 h + 16 g + 8 u ..
+  u32x4 q[2 * KD];
+#pragma unroll
+  for (int h = 0; h < KD; ++h)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      q[2 * h + u] = *reinterpret_cast<const u32x4*>(a.q + tok * a.ldq + qh * a.hdq + 64 * h + 16 * g + 8 * u);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q[2 * h + u][i] ^= flip;
     }
-    float mt = z;
-    for (int o = 32; o >= 1; o >>= 1) mt = fmaxf(mt, __shfl_xor(mt, o));
-    const float mn = fmaxf(m, mt);
-    const float base = mn == -INFINITY ? 0.0f : mn;
-    const float fade = expf(m - base);
-    const float p = expf(z - base);
-    float sum = p;
-    for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o);
-    l = l * fade + sum;
-    m = mn;
-    for (int e = 0; e < E; ++e) y[e] *= fade;
-    for (int t = 0; t < 64; ++t) {
-      const int32_t pt = __shfl(pg, t);
-      if (pt < 0) continue;
-      const float w = __shfl(p, t) * __shfl(vs, t);
-      const uint8_t* v = a.vc + ((int64_t(pt) * a.p.heads + head) * page + (j0 + t) % page) * D + lane * E;
-      for (int e = 0; e < E; ++e) {
-        float x[4];
-        decode4<F>(v[e], x);
-        y[e] += w * x[0];
+  f32x4 o[DT] = {};
+  float m = -INFINITY, l = 0.0f;
+
+  struct Step {
+    u32x4 k[2][KD];
+    uint32_t v[8][VW];
+    int32_t pg[2];
+    float ks[2], vs[2];
+  };
+  auto load = [&](Step& st, int32_t k0) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int32_t p0 = k0 + 16 * t, lp = p0 / page;
+      st.pg[t] = p0 < part.hi ? page_of(a.p, b, lp) : -1;
+      const int64_t at = int64_t(st.pg[t] < 0 ? 0 : st.pg[t]) * heads + head;
+      st.ks[t] = a.ks[at];
+      st.vs[t] = a.vs[at];
+      const int64_t base = (at * page + (p0 - lp * page)) * D;
+#pragma unroll
+      for (int h = 0; h < KD; ++h)
+        st.k[t][h] = *reinterpret_cast<const u32x4*>(a.kc + base + c * D + 64 * h + 16 * g);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint8_t* p = a.vc + base + (4 * g + j) * D + c * (D / 16);
+        if constexpr (VW == 2) {
+          const u32x2 x = *reinterpret_cast<const u32x2*>(p);
+          st.v[4 * t + j][0] = x[0];
+          st.v[4 * t + j][1] = x[1];
+        } else {
+          st.v[4 * t + j][0] = *reinterpret_cast<const uint32_t*>(p);
+        }
       }
     }
+  };
+
+  const int32_t begin = part.lo + 32 * wave;
+  Step cur;
+  if (begin < part.hi) load(cur, begin);
+  for (int32_t k0 = begin; k0 < part.hi; k0 += 32 * W) {
+    Step next;
+    load(next, k0 + 32 * W < part.hi ? k0 + 32 * W : k0);
+    f32x4 z[2];
+    PartScale ps[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      z[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int h = 0; h < KD; ++h)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          z[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              __builtin_bit_cast(bf16x8, bf16_of<F>(cur.k[t][h][2 * u], cur.k[t][h][2 * u + 1])),
+              __builtin_bit_cast(bf16x8, q[2 * h + u]), z[t], 0, 0, 0);
+      ps[t] = part_scale(cur.pg[t], cur.ks[t], cur.vs[t], sm);
+    }
+    const bool edge = k0 < all_lo || k0 + 32 > all_hi || k0 + 32 > part.hi || cur.pg[0] < 0 || cur.pg[1] < 0;
+    uint32_t seen = 0xFFu;  // bit 4 t + i: this lane's row sees key 16 t + 4 g + i
+    uint32_t odd = 0;       // some value code is not finite, in a step that not every row sees whole
+    if (edge) {
+      seen = 0;
+      uint32_t held = 0;    // keys that some row sees
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int32_t j = k0 + 16 * t + 4 * g + i;
+          const bool there = cur.pg[t] >= 0 && j < part.hi;
+          if (there && j >= see.lo && j < see.hi) seen |= 1u << (4 * t + i);
+          if (there && j >= any_lo) held |= 1u << (4 * t + i);
+          if (!(seen >> (4 * t + i) & 1)) z[t][i] = -INFINITY;
+        }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int w = 0; w < VW; ++w) {
+          if (!(held >> j & 1)) cur.v[j][w] = 0;
+          odd |= non_finite<F>(cur.v[j][w]);
+        }
+    }
+    float top = -INFINITY;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      top = fmaxf(top, fmaf(fmaxf(fmaxf(z[t][0], z[t][1]), fmaxf(z[t][2], z[t][3])), ps[t].c, ps[t].lv));
+    if (__any(top > m + kSlack)) {
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const float mn = fmaxf(m, top);
+      const float fade = mn == -INFINITY ? 1.0f : exp2_fast(m - mn);
+      l *= fade;
+#pragma unroll
+      for (int d = 0; d < DT; ++d) o[d] *= fade;
+      m = mn;
+    }
+    const float base = m == -INFINITY ? 0.0f : m;
+    float w[8];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const float shift = ps[t].lv - base;
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float e = exp2_fast(fmaf(z[t][i], ps[t].c, shift));
+        w[4 * t + i] = seen >> (4 * t + i) & 1 ? e : 0.0f;
+        sum += w[4 * t + i];
+      }
+      l = fmaf(sum, ps[t].inv, l);
+    }
+    const u32x4 pw = u32x4{pack_f16(w[0], w[1]), pack_f16(w[2], w[3]), pack_f16(w[4], w[5]), pack_f16(w[6], w[7])};
+    const f16x8 pf = __builtin_bit_cast(f16x8, pw);
+    // value operands of the 16-wide tiles of dword x: key pairs of each byte
+    auto values = [&](int x, u32x4* out) {
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        const uint32_t a0 = to_f16<F, false>(cur.v[j][x]), a1 = to_f16<F, true>(cur.v[j][x]);
+        const uint32_t b0 = to_f16<F, false>(cur.v[j + 1][x]), b1 = to_f16<F, true>(cur.v[j + 1][x]);
+        out[0][j / 2] = __builtin_amdgcn_perm(b0, a0, 0x05040100u);
+        out[1][j / 2] = __builtin_amdgcn_perm(b0, a0, 0x07060302u);
+        out[2][j / 2] = __builtin_amdgcn_perm(b1, a1, 0x05040100u);
+        out[3][j / 2] = __builtin_amdgcn_perm(b1, a1, 0x07060302u);
+      }
+    };
+    if (!__any(odd != 0) && ps[0].kind <= kFine && ps[1].kind <= kFine) {
+#pragma unroll
+      for (int x = 0; x < VW; ++x) {
+        u32x4 vf[4];
+        values(x, vf);
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+          o[4 * x + d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, vf[d]), pf, o[4 * x + d], 0, 0, 0);
+      }
+    } else {
+      // Key by key, each row taking the sum only if it sees the key: 0 * NaN
+      // of a hidden key stays out.
+      for (int key = 0; key < 32; ++key) {
+        const int kg = (key & 15) >> 2, ks = (key >> 4) * 4 + (key & 3);  // lane group and slot that hold it
+        const bool mine = __shfl(static_cast<int>(seen), kg * 16 + c) >> ks & 1;
+#pragma unroll
+        for (int x = 0; x < VW; ++x) {
+          u32x4 vf[4];
+          values(x, vf);
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+              if (ps[p / 2].kind > kFine) vf[d][p] = blown_up(vf[d][p], ps[p / 2].kind);
+              vf[d][p] = g == kg && ks / 2 == p ? vf[d][p] & (ks & 1 ? 0xFFFF0000u : 0x0000FFFFu) : 0u;
+            }
+            const f32x4 sum =
+                __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, vf[d]), pf, o[4 * x + d], 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[4 * x + d][i] = mine ? sum[i] : o[4 * x + d][i];
+          }
+        }
+      }
+    }
+    cur = next;
+  }
+  // join the waves; o[4 x + d][i] is dimension (D/16) (4 g + i) + 4 x + d of row c
+  l += __shfl_xor(l, 16);
+  l += __shfl_xor(l, 32);
+  if (g == 0) sh_ml[wave][c] = make_float2(m, l);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int x = 0; x < VW; ++x)
+      *reinterpret_cast<f32x4*>(&sh_o[wave][c][(D / 16) * (4 * g + i) + 4 * x]) =
+          f32x4{o[4 * x][i], o[4 * x + 1][i], o[4 * x + 2][i], o[4 * x + 3][i]};
+  __syncthreads();
+  for (int e = threadIdx.x; e < rows * (D / 4); e += 64 * W) {
+    const int row = e / (D / 4), d = e % (D / 4) * 4;
+    float mt = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < W; ++w) mt = fmaxf(mt, sh_ml[w][row].x);
+    const float base = mt == -INFINITY ? 0.0f : mt;
+    float lt = 0.0f;
+    f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float2 ml = sh_ml[w][row];
+      const float f = exp2_fast(ml.x - base);
+      lt += ml.y * f;
+      y += *reinterpret_cast<const f32x4*>(&sh_o[w][row][d]) * f;
+    }
+    const int32_t rr = r0 + row;
+    const int64_t t = s.tok0 + rr / group, h = int64_t(head) * group + rr % group;
+    if (cut.chunks == 1) {
+      const float inv = lt != 0.0f ? 1.0f / lt : 0.0f;
+      *reinterpret_cast<u32x2*>(a.y + t * a.ldy + h * a.hdy + d) =
+          u32x2{pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv)};
+      if (a.lse && d == 0) a.lse[t * a.q_heads + h] = lt != 0.0f ? (base + log2_fast(lt)) * kLn2 : -INFINITY;
+    } else {
+      const int64_t at = (int64_t(chunk) * a.p.tokens + t) * a.q_heads + h;
+      *reinterpret_cast<f32x4*>(parts.o + at * D + d) = y;
+      if (d == 0) parts.ml[at] = make_float2(mt, lt);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// 128 query rows a workgroup, 32 a wave: prompts and chunks of prompts.  Tiles of 64 keys
+// are widened once into LDS (keys to bf16, values to fp16) while the tile before is computed
+// from the other buffer, one barrier a tile.  Rows of 2 D bytes are
+// stored with their 16-byte (keys) or 64-byte (values) pieces permuted by the key, so that the
+// operand reads -- 16 bytes of 16 keys; 8 bytes of 4 keys, transposed by ds_read_b64_tr_b16 --
+// touch every bank once.
+constexpr int kBK = 64;
+
+template <int D>
+__device__ __forceinline__ int key_at(int key, int piece) {  // byte offset of a 16-byte piece of a key
+  const int x = D == 128 ? (key & 15) : ((key >> 1) & 7);
+  return key * (2 * D) + ((piece ^ x) << 4);
+}
+template <int D>
+__device__ __forceinline__ int val_at(int key, int byte) {  // byte offset of a byte of a value row
+  const int x = D == 128 ? (key & 3) : ((key >> 1) & 1);
+  return key * (2 * D) + (byte ^ (x << 6));
+}
+
+__device__ __forceinline__ u32x2 read_tr(const uint8_t* p) {
+  const i16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+      (__attribute__((address_space(3))) i16x4*)(p));
+  return __builtin_bit_cast(u32x2, v);
+}
+
+template <int F, int D>
+__global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs a, Cut cut, int32_t tiles, Parts parts) {
+  constexpr int NP = D / 64;   // 16-byte pieces of keys, and of values, that a thread stages
+  constexpr int KS = D / 16;   // matrix steps along the dimensions
+  constexpr int DT = D / 32;   // 32-wide output tiles
+  __shared__ __align__(16) uint8_t sh_k[2][kBK * D * 2];
+  __shared__ __align__(16) uint8_t sh_v[2][kBK * D * 2];
+  __shared__ __align__(16) float4 sh_p[2][4];  // PartScale of the tile's 16-key parts
+  __shared__ int sh_odd[2];                    // the last tile of this buffer with a value code that is not finite
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = lane & 31, h = lane >> 5;
+  const int32_t heads = a.p.heads, group = static_cast<int32_t>(a.q_heads / heads);
+  int64_t blk = blockIdx.x;
+  const int32_t head = static_cast<int32_t>(blk % heads);
+  blk /= heads;
+  const int32_t r0 = (tiles - 1 - static_cast<int32_t>(blk % tiles)) * 128;  // causal: the longest first
+  blk /= tiles;
+  const int32_t chunk = static_cast<int32_t>(blk % cut.chunks);
+  const int64_t b = blk / cut.chunks;
+  const SeqSpan s = seq_span(a.p, b);
+  const int64_t all = int64_t(s.n) * group;
+  if (r0 >= all) return;
+  const int32_t rows = all - r0 < 128 ? static_cast<int32_t>(all - r0) : 128;
+  const Range tile = tile_range(a, s, r0, rows, group);
+  const Range part = chunk_of(tile, cut, chunk);
+  if (chunk > 0 && part.lo >= part.hi) return;
+  const int32_t page = a.p.page;
+  const int32_t any_lo = visible(a, s, r0 / group).lo;
+
+  // this lane's query row, and what all rows of this wave see / any of them sees
+  const int32_t wr = rows - 32 * wave < 32 ? rows - 32 * wave : 32;  // rows of this wave (may be <= 0)
+  const int32_t r = r0 + 32 * wave + (c < wr ? c : 0);
+  const int64_t tok = s.tok0 + (wr > 0 ? r / group : 0);
+  const int64_t qh = int64_t(head) * group + r % group;
+  Range see = {0, 0}, w_all = {0, 0}, w_any = {0, 0};
+  if (wr > 0) {
+    const Range f = visible(a, s, (r0 + 32 * wave) / group), e = visible(a, s, (r0 + 32 * wave + wr - 1) / group);
+    w_all = Range{e.lo, f.hi};
+    w_any = Range{f.lo, e.hi};
+    if (c < wr) see = visible(a, s, r / group);
+  }
+  const float sm = fabsf(a.sm_scale) * kLog2e;
+  const uint32_t flip = a.sm_scale < 0.0f ? 0x80008000u : 0u;
+  u32x4 q[KS];
+#pragma unroll
+  for (int i = 0; i < KS; ++i) {
+    q[i] = *reinterpret_cast<const u32x4*>(a.q + tok * a.ldq + qh * a.hdq + 16 * i + 8 * h);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) q[i][j] ^= flip;
+  }
+  f32x16 o[DT] = {};
+  float m = -INFINITY, l = 0.0f;
+
+  // staging: this thread's pieces are bytes [16 sp, 16 sp + 16) of keys sk + 64 / NP * i
+  constexpr int TK = D / 16;  // threads of a key
+  const int sk = threadIdx.x / TK, sp = threadIdx.x % TK;
+  u32x4 kr[NP], vr[NP];
+  float4 pr;
+  auto fetch = [&](int32_t k0) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int32_t j = k0 + sk + (kBK / NP) * i, lp = j / page;
+      const int32_t pg = j < part.hi ? page_of(a.p, b, lp) : -1;
+      const bool held = pg >= 0 && j >= any_lo;
+      const int64_t at = ((int64_t(pg < 0 ? 0 : pg) * heads + head) * page + (j - lp * page)) * D + 16 * sp;
+      kr[i] = *reinterpret_cast<const u32x4*>(a.kc + at);
+      vr[i] = *reinterpret_cast<const u32x4*>(a.vc + at);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) vr[i][e] = held ? vr[i][e] : 0u;  // what no row sees counts for nothing
+    }
+    if (threadIdx.x < 4) {
+      const int32_t j = k0 + 16 * threadIdx.x;
+      const int32_t pg = j < part.hi ? page_of(a.p, b, j / page) : -1;
+      const int64_t at = int64_t(pg < 0 ? 0 : pg) * heads + head;
+      const PartScale ps = part_scale(pg, a.ks[at], a.vs[at], sm);
+      pr = make_float4(ps.c, ps.lv, ps.inv, static_cast<float>(ps.kind));
+    }
+  };
+  auto stage = [&](int buf, int index) {
+    uint32_t odd = 0;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int key = sk + (kBK / NP) * i;
+      *reinterpret_cast<u32x4*>(sh_k[buf] + key_at<D>(key, 2 * sp)) = bf16_of<F>(kr[i][0], kr[i][1]);
+      *reinterpret_cast<u32x4*>(sh_k[buf] + key_at<D>(key, 2 * sp + 1)) = bf16_of<F>(kr[i][2], kr[i][3]);
+      u32x4* v = reinterpret_cast<u32x4*>(sh_v[buf] + val_at<D>(key, 32 * sp));
+      v[0] = f16_of<F>(vr[i][0], vr[i][1]);
+      v[1] = f16_of<F>(vr[i][2], vr[i][3]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) odd |= non_finite<F>(vr[i][e]);
+    }
+    if (odd) sh_odd[buf] = index;
+    if (threadIdx.x < 4) sh_p[buf][threadIdx.x] = pr;
+  };
+  const int32_t steps = (part.hi - part.lo + kBK - 1) / kBK;
+  if (threadIdx.x < 2) sh_odd[threadIdx.x] = -1;
+  __syncthreads();
+  if (steps > 0) {
+    fetch(part.lo);
+    stage(0, 0);
+  }
+  __syncthreads();
+  for (int32_t t = 0; t < steps; ++t) {
+    const int buf = t & 1;
+    const int32_t k0 = part.lo + kBK * t;
+    if (t + 1 < steps) fetch(k0 + kBK);
+    if (k0 < w_any.hi && k0 + kBK > w_any.lo) {
+      f32x16 z[2];
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt) {
+        z[kt] = f32x16{};
+#pragma unroll
+        for (int i = 0; i < KS; ++i)
+          z[kt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+              *reinterpret_cast<const bf16x8*>(sh_k[buf] + key_at<D>(32 * kt + c, 2 * i + h)),
+              __builtin_bit_cast(bf16x8, q[i]), z[kt], 0, 0, 0);
+      }
+      float4 ps[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ps[i] = sh_p[buf][i];
+      const float kind_lo = fminf(fminf(ps[0].w, ps[1].w), fminf(ps[2].w, ps[3].w));
+      const float kind_hi = fmaxf(fmaxf(ps[0].w, ps[1].w), fmaxf(ps[2].w, ps[3].w));
+      const bool edge = k0 < w_all.lo || k0 + kBK > w_all.hi || k0 + kBK > part.hi || kind_lo == kAbsent;
+      // register 8 e + i of part 2 kt + e is key 32 kt + 16 e + 8 (i / 4) + 4 h + i % 4
+      uint32_t seen[2] = {0xFFFFu, 0xFFFFu};
+      if (edge) {
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt) {
+          seen[kt] = 0;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int32_t j = k0 + 32 * kt + 8 * (i / 4) + 4 * h + i % 4;
+            const bool v = j >= see.lo && j < see.hi && j < part.hi && ps[2 * kt + i / 8].w != kAbsent;
+            seen[kt] |= v ? 1u << i : 0u;
+            z[kt][i] = v ? z[kt][i] : -INFINITY;
+          }
+        }
+      }
+      float top = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float x = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x = fmaxf(x, z[e / 2][8 * (e % 2) + i]);
+        top = fmaxf(top, fmaf(x, ps[e].x, ps[e].y));
+      }
+      if (__any(top > m + kSlack)) {
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float mn = fmaxf(m, top);
+        const float fade = mn == -INFINITY ? 1.0f : exp2_fast(m - mn);
+        l *= fade;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) o[d] *= fade;
+        m = mn;
+      }
+      const float base = m == -INFINITY ? 0.0f : m;
+      f16x8 pf[4];  // weights of the tile's 16-key parts
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float shift = ps[e].y - base;
+        float w[8];
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = exp2_fast(fmaf(z[e / 2][8 * (e % 2) + i], ps[e].x, shift));
+        if (edge) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[i] = seen[e / 2] >> (8 * (e % 2) + i) & 1 ? w[i] : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum += w[i];
+        l = fmaf(sum, ps[e].z, l);
+        pf[e] = __builtin_bit_cast(f16x8, (u32x4{pack_f16(w[0], w[1]), pack_f16(w[2], w[3]), pack_f16(w[4], w[5]),
+                                                 pack_f16(w[6], w[7])}));
+      }
+      // values of part e, output tile d: keys 16 e + {0..3, 8..11} + 4 h, dimension 32 d + c
+      auto values = [&](int e, int d) {
+        const int key = 16 * e + 4 * h + (lane & 15) / 4, byte = 64 * d + 32 * ((lane >> 4) & 1) + 8 * (lane & 3);
+        const u32x2 lo = read_tr(sh_v[buf] + val_at<D>(key, byte)), hi = read_tr(sh_v[buf] + val_at<D>(key + 8, byte));
+        return u32x4{lo[0], lo[1], hi[0], hi[1]};
+      };
+      if (!(edge && sh_odd[buf] == t) && kind_hi <= kFine) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int d = 0; d < DT; ++d)
+            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, values(e, d)), pf[e], o[d], 0, 0, 0);
+      } else {
+        // key by key, each row taking the sum only if it sees the key
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          for (int key = 0; key < 16; ++key) {
+            const int kh = (key >> 2) & 1, slot = (key >> 3) * 4 + (key & 3);  // lane half and slot that hold it
+            const int32_t j = k0 + 16 * e + key;
+            const bool mine = j >= see.lo && j < see.hi && j < part.hi && ps[e].w != kAbsent;
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+              u32x4 v = values(e, d);
+#pragma unroll
+              for (int p = 0; p < 4; ++p) {
+                if (ps[e].w > kFine) v[p] = blown_up(v[p], static_cast<int>(ps[e].w));
+                v[p] = h == kh && slot / 2 == p ? v[p] & (slot & 1 ? 0xFFFF0000u : 0x0000FFFFu) : 0u;
+              }
+              const f32x16 sum =
+                  __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, v), pf[e], o[d], 0, 0, 0);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[d][i] = mine ? sum[i] : o[d][i];
+            }
+          }
+        }
+      }
+    }
+    if (t + 1 < steps) stage(buf ^ 1, t + 1);
+    __syncthreads();
+  }
+  l += __shfl_xor(l, 32);
+  if (c >= wr) return;
+  const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+  const int64_t at = (int64_t(chunk) * a.p.tokens + tok) * a.q_heads + qh;
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int dim = 32 * d + 8 * i + 4 * h;
+      const f32x4 y = {o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
+      if (cut.chunks == 1)
+        *reinterpret_cast<u32x2*>(a.y + tok * a.ldy + qh * a.hdy + dim) =
+            u32x2{pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv)};
+      else
+        *reinterpret_cast<f32x4*>(parts.o + at * D + dim) = y;
+    }
+  if (h == 0) {
+    if (cut.chunks > 1)
+      parts.ml[at] = make_float2(m, l);
+    else if (a.lse)
+      a.lse[tok * a.q_heads + qh] = l != 0.0f ? (m + log2_fast(l)) * kLn2 : -INFINITY;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Adds the chunks of each query row (one wave a row): with M = max m_i,
+// y = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.
+template <int D>
+__global__ void __launch_bounds__(256) k_attend_join(AttendArgs a, Cut cut, int32_t tile_rows, Parts parts) {
+  constexpr int E = D / 64;
+  const int lane = threadIdx.x & 63;
+  const int64_t b = blockIdx.y;
+  const int32_t group = static_cast<int32_t>(a.q_heads / a.p.heads);
+  const SeqSpan s = seq_span(a.p, b);
+  const int64_t x = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);  // (token, q head) of the sequence
+  const int64_t i = x / a.q_heads, h = x % a.q_heads;
+  if (i >= s.n) return;
+  const int32_t r0 = static_cast<int32_t>((i * group + h % group) / tile_rows * tile_rows);
+  const int64_t left = int64_t(s.n) * group - r0;
+  const Range tile = tile_range(a, s, r0, left < tile_rows ? static_cast<int32_t>(left) : tile_rows, group);
+  int64_t n = (int64_t(tile.hi) - tile.lo + cut.len - 1) / cut.len;
+  n = n < 1 ? 1 : n > cut.chunks ? cut.chunks : n;
+  const int64_t tok = s.tok0 + i, row = tok * a.q_heads + h, step = a.p.tokens * a.q_heads;
+  float top = -INFINITY;
+  for (int64_t k = lane; k < n; k += 64) top = fmaxf(top, parts.ml[k * step + row].x);
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+  const float base = top == -INFINITY ? 0.0f : top;
+  float l = 0.0f, y[E] = {};
+#pragma unroll 4
+  for (int64_t k = 0; k < n; ++k) {
+    const float2 ml = parts.ml[k * step + row];
+    const float f = exp2_fast(ml.x - base);
+    l += ml.y * f;
+    const float* o = parts.o + (k * step + row) * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) y[e] += o[e] * f;
   }
   const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-  for (int e = 0; e < E; ++e) {
-    const __bf16 r = static_cast<__bf16>(y[e] * inv);
-    a.y[tok * a.ldy + h * a.hdy + lane * E + e] = __builtin_bit_cast(uint16_t, r);
-  }
-  if (a.lse && lane == 0) a.lse[tok * a.q_heads + h] = l != 0.0f ? m + logf(l) : -INFINITY;
+  uint16_t* out = a.y + tok * a.ldy + h * a.hdy + lane * E;
+  if constexpr (E == 2)
+    *reinterpret_cast<uint32_t*>(out) = pack_bf16(y[0] * inv, y[1] * inv);
+  else
+    *out = static_cast<uint16_t>(pack_bf16(y[0] * inv, 0.0f));
+  if (a.lse && lane == 0) a.lse[row] = l != 0.0f ? (base + log2_fast(l)) * kLn2 : -INFINITY;
 }
 
 }  // namespace
 
 hipError_t launch_paged_attention(const AttendArgs& a, hipStream_t st) {
-  const int64_t gx = a.p.seqs * a.p.max_new;
-  if (gx >= (int64_t(1) << 26)) return hipErrorInvalidValue;
-  const dim3 grid(static_cast<uint32_t>(gx), static_cast<uint32_t>(a.q_heads));
-  auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, dim3(64), 0, st, a, a.p.max_new); };
+  const int64_t group = a.q_heads / a.p.heads;
+  const int64_t rows = a.p.max_new * group;
+  const bool few = rows <= 16;
+  const int64_t tile_rows = few ? 16 : 128;
+  const int64_t tiles = ceil_div(rows, tile_rows);
+  const int64_t jobs = a.p.seqs * tiles * a.p.heads;  // workgroups without a cut
+  // Cut the keys when the jobs alone do not fill the card: chunks of at least 512 keys, about 8 workgroups per CU.
+  Cut cut{1, 64};
+  const int64_t want = ceil_div(int64_t(8) * device_cus(), jobs);
+  if (want > 1) {
+    const int64_t len = std::max<int64_t>(512, ceil_div(ceil_div(a.max_kv, want), 64) * 64);
+    cut.chunks = static_cast<int32_t>(ceil_div(a.max_kv, len));
+    cut.len = static_cast<int32_t>(len);
+  }
+  Parts parts{nullptr, nullptr};
+  if (cut.chunks > 1) {
+    const size_t n = size_t(cut.chunks) * a.p.tokens * a.q_heads;
+    void* p = nullptr;
+    const hipError_t e = get_scratch(st, n * (a.p.dim + 2) * sizeof(float), &p);
+    if (e != hipSuccess) return e;
+    parts.o = static_cast<float*>(p);
+    parts.ml = reinterpret_cast<float2*>(parts.o + n * a.p.dim);
+  }
+  const int64_t grid = jobs * cut.chunks;
+  const int32_t nt = static_cast<int32_t>(tiles);
+  auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(grid), dim3(256), 0, st, a, cut, nt, parts); };
+  auto by_dim = [&](auto f) {
+    constexpr int F = decltype(f)::value;
+    if (few)
+      a.p.dim == 128 ? go(k_attend_few<F, 128, 4>) : go(k_attend_few<F, 64, 4>);
+    else
+      a.p.dim == 128 ? go(k_attend_many<F, 128>) : go(k_attend_many<F, 64>);
+  };
   if (a.p.fmt == FP8RT_E4M3)
-    a.p.dim == 128 ? go(k_attend<kE4M3, 128>) : go(k_attend<kE4M3, 64>);
+    by_dim(std::integral_constant<int, kE4M3>{});
   else
-    a.p.dim == 128 ? go(k_attend<kE5M2, 128>) : go(k_attend<kE5M2, 64>);
-  return hipGetLastError();
+    by_dim(std::integral_constant<int, kE5M2>{});
+  hipError_t e = hipGetLastError();
+  if (e == hipSuccess && cut.chunks > 1) {
+    const dim3 jg(static_cast<uint32_t>(ceil_div(a.p.max_new * a.q_heads, 4)), static_cast<uint32_t>(a.p.seqs));
+    auto join = [&](auto kern) {
+      hipLaunchKernelGGL(kern, jg, dim3(256), 0, st, a, cut, static_cast<int32_t>(tile_rows), parts);
+    };
+    a.p.dim == 128 ? join(k_attend_join<128>) : join(k_attend_join<64>);
+    e = hipGetLastError();
+  }
+  return e;
 }
 
 }  // namespace fp8rt

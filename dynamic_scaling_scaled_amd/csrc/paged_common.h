@@ -25,7 +25,8 @@ __device__ __forceinline__ SeqSpan seq_span(const PagedArgs& p, int64_t b) {
   s.tok0 = t0;
   s.first = len - (t1 - t0);
   s.n = static_cast<int32_t>(t1 - t0 < p.max_new ? t1 - t0 : p.max_new);
-  const int64_t cap = p.ld_table * p.page;
+  // positions stay 32-bit with room for a tile past the end
+  const int64_t cap = p.ld_table * p.page < 0x7FFF0000 ? p.ld_table * p.page : 0x7FFF0000;
   s.len = len < 0 ? 0 : len < cap ? len : cap;
   return s;
 }

@@ -509,7 +509,7 @@ fp8rt_status fp8_rmsnorm_backward(const void* dy, fp8rt_dtype dyt, int64_t rows,
  * bound every index by tokens, pages, ld_table and max_new.  A table entry outside
  * [0, pages) stands for a page that is not there (nothing is written to it,
  * attention takes its positions as hidden); positions past ld_table *
- * page_size and before 0 are dropped in the same way, and so are tokens past max_new.
+ * page_size (or 2^31 - 2^16) and before 0 are dropped in the same way, and so are tokens past max_new.
  *
  * fp8_kv_append writes the new tokens' keys and values into the cache.  For
  * each page and head that receives tokens, a = max |x| over what it receives:
@@ -549,7 +549,9 @@ fp8rt_status fp8_kv_append(const void* k, const void* v, fp8rt_dtype xt, int64_t
  *   lse : nullable fp32 [tokens][q_heads]: m + ln(sum_j e^(z[j] - m))
  *   max_kv : a bound on kv_len (host), used to choose how the work is split; longer
  *            sequences are still computed
- * q_heads a multiple of heads; sm_scale finite; window >= 0.
+ * The scales are those fp8_kv_append writes: positive, or NaN.
+ * q_heads a multiple of heads; sm_scale finite; window >= 0; at most 2^23 tiles of
+ * 128 (token, head of a group) rows over all sequences and heads (else FP8RT_EUNSUPPORTED).
  * Alignment: ldq, hdq multiples of 8, ldy, hdy of 4, q and the caches 16-byte, y 8-byte aligned.
  * Scratch: the per-stream scratch buffer holds the parts of sequences split along their keys. */
 fp8rt_status fp8_paged_attention(const void* q, fp8rt_dtype qt, int64_t tokens, int64_t q_heads, int64_t ldq,
