@@ -136,30 +136,93 @@ struct Parts {
 };
 
 // What one 16-key part of a step needs from its page: t = dot * c, log2 of the v scale, its inverse.
-// A v scale that is not finite counts as 1 here (scores and sums do not depend on
-// it); its values are put right by blown_up on the way that takes such steps.
-constexpr int kAbsent = 0, kFine = 1, kNaNScale = 2, kInfScale = 3;
+// A v scale that is not finite counts as 1 here, and the rows are done again by careful_row.
+constexpr int kAbsent = 0, kFine = 1, kNotFinite = 2;
 struct PartScale {
   float c, lv, inv;
   int kind;
 };
 __device__ __forceinline__ PartScale part_scale(int32_t pg, float ks, float vs, float sm) {
-  const bool nan = __builtin_isnan(vs), inf = vs > 3.4028235e38f;
-  const float v = nan || inf ? 1.0f : vs < kTinyScale ? kTinyScale : vs;
-  return PartScale{ks * sm, log2_fast(v), 1.0f / v, pg < 0 ? kAbsent : nan ? kNaNScale : inf ? kInfScale : kFine};
+  const bool fine = vs <= 3.4028235e38f;
+  const float v = !fine ? 1.0f : vs < kTinyScale ? kTinyScale : vs;
+  return PartScale{ks * sm, log2_fast(v), 1.0f / v, pg < 0 ? kAbsent : fine ? kFine : kNotFinite};
 }
 
-// Two fp16 code values under a scale that is NaN or infinite: NaN, or an
-// infinity of the code's sign (0 * Inf is NaN).
-__device__ __forceinline__ uint32_t blown_up(uint32_t x, int kind) {
-  uint32_t r = 0;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t v = x >> (16 * i) & 0xFFFFu, mag = v & 0x7FFFu;
-    const uint32_t y = kind == kNaNScale || mag == 0 || mag > 0x7C00u ? 0x7E00u : (v & 0x8000u) | 0x7C00u;
-    r |= y << (16 * i);
+// One query row over the keys [see.lo, see.hi), by one wave, without products that hidden keys take
+// part in: m, l = sum 2^(t - m) and this lane's D/64 dimensions of sum 2^(t - m) v.  The matrix
+// kernels multiply a hidden key's value by a weight of 0, which is not 0 for a NaN or an infinity; they
+// notice such codes and scales and take this slow way for the rows concerned, after their loop
+// (inside it, it would cost the registers that keep the accumulators out of memory).
+template <int F, int D>
+__device__ void careful_row(const AttendArgs& a, int64_t b, int32_t head, int64_t tok, int64_t qh, Range see, float& m,
+                            float& l, float* y) {
+  constexpr int E = D / 64;
+  const int lane = threadIdx.x & 63;
+  const int32_t page = a.p.page;
+  const uint16_t* q = a.q + tok * a.ldq + qh * a.hdq;
+  const float sm = a.sm_scale * kLog2e;
+  m = -INFINITY;
+  l = 0.0f;
+  for (int e = 0; e < E; ++e) y[e] = 0.0f;
+  for (int32_t j0 = see.lo; j0 < see.hi; j0 += 64) {
+    const int32_t j = j0 + lane;
+    const int32_t pg = j < see.hi ? page_of(a.p, b, j / page) : -1;
+    const int64_t at = int64_t(pg < 0 ? 0 : pg) * a.p.heads + head;
+    const int64_t base = (at * page + j % page) * D;
+    float t = -INFINITY;
+    if (pg >= 0) {
+      float dot = 0.0f;
+      for (int d = 0; d < D; d += 4) {
+        float v[4];
+        decode4<F>(*reinterpret_cast<const uint32_t*>(a.kc + base + d), v);
+        for (int i = 0; i < 4; ++i) dot = fmaf(v[i], __uint_as_float(static_cast<uint32_t>(q[d + i]) << 16), dot);
+      }
+      t = dot * (a.ks[at] * sm);
+    }
+    float top = t;
+    for (int d = 32; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+    const float mn = fmaxf(m, top), ref = mn == -INFINITY ? 0.0f : mn;
+    const float fade = exp2_fast(m - ref), w = exp2_fast(t - ref);
+    float sum = w;
+    for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
+    l = l * fade + sum;
+    m = mn;
+    for (int e = 0; e < E; ++e) y[e] *= fade;
+    const float vs = a.vs[at];
+    for (int k = 0; k < 64; ++k) {
+      if (__shfl(pg, k) < 0) continue;
+      const int64_t from = int64_t(__shfl(static_cast<int>(base >> 32), k)) << 32 |
+                           static_cast<uint32_t>(__shfl(static_cast<int>(base), k));
+      const float wk = __shfl(w, k), sk = __shfl(vs, k);
+      for (int e = 0; e < E; ++e) {
+        float v[4];
+        decode4<F>(a.vc[from + lane * E + e], v);
+        y[e] += wk * (sk * v[0]);
+      }
+    }
   }
-  return r;
+}
+
+// Writes such a row: the output (one chunk) or its part.
+template <int D>
+__device__ void careful_store(const AttendArgs& a, const Parts& parts, int32_t chunks, int32_t chunk, int64_t tok,
+                              int64_t qh, float m, float l, const float* y) {
+  constexpr int E = D / 64;
+  const int lane = threadIdx.x & 63;
+  const int64_t at = (int64_t(chunk) * a.p.tokens + tok) * a.q_heads + qh;
+  const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+  for (int e = 0; e < E; ++e) {
+    if (chunks == 1)
+      a.y[tok * a.ldy + qh * a.hdy + lane * E + e] = static_cast<uint16_t>(pack_bf16(y[e] * inv, 0.0f));
+    else
+      parts.o[at * D + lane * E + e] = y[e];
+  }
+  if (lane == 0) {
+    if (chunks > 1)
+      parts.ml[at] = make_float2(m, l);
+    else if (a.lse)
+      a.lse[tok * a.q_heads + qh] = l != 0.0f ? (m + log2_fast(l)) * kLn2 : -INFINITY;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -178,6 +241,7 @@ __global__ void __launch_bounds__(64 * W, W == 4 ? 3 : 1)
   constexpr int LD = D + 4;
   __shared__ __align__(16) float sh_o[W][16][LD];
   __shared__ float2 sh_ml[W][16];
+  __shared__ int sh_redo[W];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = lane & 15, g = lane >> 4;
   const int32_t heads = a.p.heads, group = static_cast<int32_t>(a.q_heads / heads);
@@ -195,7 +259,7 @@ __global__ void __launch_bounds__(64 * W, W == 4 ? 3 : 1)
   const Range tile = tile_range(a, s, r0, rows, group);
   const Range part = chunk_of(tile, cut, chunk);
   if (chunk > 0 && part.lo >= part.hi) return;  // (chunk 0 also writes the rows that see nothing)
-  const int32_t page = a.p.page;
+  const int32_t page = a.p.page, shift = 31 - __builtin_clz(page);
   // this lane's query row
   const int32_t r = r0 + (c < rows ? c : 0);
   const int64_t tok = s.tok0 + r / group;
@@ -229,7 +293,7 @@ __global__ void __launch_bounds__(64 * W, W == 4 ? 3 : 1)
   auto load = [&](Step& st, int32_t k0) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const int32_t p0 = k0 + 16 * t, lp = p0 / page;
+      const int32_t p0 = k0 + 16 * t, lp = p0 >> shift;
       st.pg[t] = p0 < part.hi ? page_of(a.p, b, lp) : -1;
       const int64_t at = int64_t(st.pg[t] < 0 ? 0 : st.pg[t]) * heads + head;
       st.ks[t] = a.ks[at];
@@ -252,6 +316,7 @@ __global__ void __launch_bounds__(64 * W, W == 4 ? 3 : 1)
     }
   };
 
+  uint32_t redo = 0;  // a hidden value, or one under such a scale, may be no finite number
   const int32_t begin = part.lo + 32 * wave;
   Step cur;
   if (begin < part.hi) load(cur, begin);
@@ -274,7 +339,6 @@ __global__ void __launch_bounds__(64 * W, W == 4 ? 3 : 1)
     }
     const bool edge = k0 < all_lo || k0 + 32 > all_hi || k0 + 32 > part.hi || cur.pg[0] < 0 || cur.pg[1] < 0;
     uint32_t seen = 0xFFu;  // bit 4 t + i: this lane's row sees key 16 t + 4 g + i
-    uint32_t odd = 0;       // some value code is not finite, in a step that not every row sees whole
     if (edge) {
       seen = 0;
       uint32_t held = 0;    // keys that some row sees
@@ -293,9 +357,10 @@ __global__ void __launch_bounds__(64 * W, W == 4 ? 3 : 1)
 #pragma unroll
         for (int w = 0; w < VW; ++w) {
           if (!(held >> j & 1)) cur.v[j][w] = 0;
-          odd |= non_finite<F>(cur.v[j][w]);
+          redo |= non_finite<F>(cur.v[j][w]);
         }
     }
+    redo |= ps[0].kind == kNotFinite || ps[1].kind == kNotFinite;
     float top = -INFINITY;
 #pragma unroll
     for (int t = 0; t < 2; ++t)
@@ -314,11 +379,11 @@ __global__ void __launch_bounds__(64 * W, W == 4 ? 3 : 1)
     float w[8];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const float shift = ps[t].lv - base;
+      const float lift = ps[t].lv - base;
       float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float e = exp2_fast(fmaf(z[t][i], ps[t].c, shift));
+        const float e = exp2_fast(fmaf(z[t][i], ps[t].c, lift));
         w[4 * t + i] = seen >> (4 * t + i) & 1 ? e : 0.0f;
         sum += w[4 * t + i];
       }
@@ -338,39 +403,13 @@ __global__ void __launch_bounds__(64 * W, W == 4 ? 3 : 1)
         out[3][j / 2] = __builtin_amdgcn_perm(b1, a1, 0x07060302u);
       }
     };
-    if (!__any(odd != 0) && ps[0].kind <= kFine && ps[1].kind <= kFine) {
 #pragma unroll
-      for (int x = 0; x < VW; ++x) {
-        u32x4 vf[4];
-        values(x, vf);
+    for (int x = 0; x < VW; ++x) {
+      u32x4 vf[4];
+      values(x, vf);
 #pragma unroll
-        for (int d = 0; d < 4; ++d)
-          o[4 * x + d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, vf[d]), pf, o[4 * x + d], 0, 0, 0);
-      }
-    } else {
-      // Key by key, each row taking the sum only if it sees the key: 0 * NaN
-      // of a hidden key stays out.
-      for (int key = 0; key < 32; ++key) {
-        const int kg = (key & 15) >> 2, ks = (key >> 4) * 4 + (key & 3);  // lane group and slot that hold it
-        const bool mine = __shfl(static_cast<int>(seen), kg * 16 + c) >> ks & 1;
-#pragma unroll
-        for (int x = 0; x < VW; ++x) {
-          u32x4 vf[4];
-          values(x, vf);
-#pragma unroll
-          for (int d = 0; d < 4; ++d) {
-#pragma unroll
-            for (int p = 0; p < 4; ++p) {
-              if (ps[p / 2].kind > kFine) vf[d][p] = blown_up(vf[d][p], ps[p / 2].kind);
-              vf[d][p] = g == kg && ks / 2 == p ? vf[d][p] & (ks & 1 ? 0xFFFF0000u : 0x0000FFFFu) : 0u;
-            }
-            const f32x4 sum =
-                __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, vf[d]), pf, o[4 * x + d], 0, 0, 0);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[4 * x + d][i] = mine ? sum[i] : o[4 * x + d][i];
-          }
-        }
-      }
+      for (int d = 0; d < 4; ++d)
+        o[4 * x + d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, vf[d]), pf, o[4 * x + d], 0, 0, 0);
     }
     cur = next;
   }
@@ -378,6 +417,8 @@ __global__ void __launch_bounds__(64 * W, W == 4 ? 3 : 1)
   l += __shfl_xor(l, 16);
   l += __shfl_xor(l, 32);
   if (g == 0) sh_ml[wave][c] = make_float2(m, l);
+  const bool wave_redo = __any(redo != 0);
+  if (lane == 0) sh_redo[wave] = wave_redo;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -385,6 +426,21 @@ __global__ void __launch_bounds__(64 * W, W == 4 ? 3 : 1)
       *reinterpret_cast<f32x4*>(&sh_o[wave][c][(D / 16) * (4 * g + i) + 4 * x]) =
           f32x4{o[4 * x][i], o[4 * x + 1][i], o[4 * x + 2][i], o[4 * x + 3][i]};
   __syncthreads();
+  int any_redo = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) any_redo |= sh_redo[w];
+  if (any_redo) {
+    for (int row = wave; row < rows; row += W) {
+      const int32_t rr = r0 + row;
+      const int64_t t = s.tok0 + rr / group, h = int64_t(head) * group + rr % group;
+      Range v = visible(a, s, rr / group);
+      v = Range{v.lo > part.lo ? v.lo : part.lo, v.hi < part.hi ? v.hi : part.hi};
+      float rm, rl, y[D / 64];
+      careful_row<F, D>(a, b, head, t, h, v, rm, rl, y);
+      careful_store<D>(a, parts, cut.chunks, chunk, t, h, rm, rl, y);
+    }
+    return;
+  }
   for (int e = threadIdx.x; e < rows * (D / 4); e += 64 * W) {
     const int row = e / (D / 4), d = e % (D / 4) * 4;
     float mt = -INFINITY;
@@ -446,8 +502,8 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs a, Cut cut, i
   constexpr int NP = D / 64;   // 16-byte pieces of keys, and of values, that a thread stages
   constexpr int KS = D / 16;   // matrix steps along the dimensions
   constexpr int DT = D / 32;   // 32-wide output tiles
-  __shared__ __align__(16) uint8_t sh_k[2][kBK * D * 2];
-  __shared__ __align__(16) uint8_t sh_v[2][kBK * D * 2];
+  constexpr int kBuf = kBK * D * 2;  // bytes of one buffer of keys, and of values
+  __shared__ __align__(16) uint8_t sh[4 * kBuf];  // keys 0, keys 1, values 0, values 1
   __shared__ __align__(16) float4 sh_p[2][4];  // PartScale of the tile's 16-key parts
   __shared__ int sh_odd[2];                    // the last tile of this buffer with a value code that is not finite
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -467,7 +523,7 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs a, Cut cut, i
   const Range tile = tile_range(a, s, r0, rows, group);
   const Range part = chunk_of(tile, cut, chunk);
   if (chunk > 0 && part.lo >= part.hi) return;
-  const int32_t page = a.p.page;
+  const int32_t page = a.p.page, shift = 31 - __builtin_clz(page);
   const int32_t any_lo = visible(a, s, r0 / group).lo;
 
   // this lane's query row, and what all rows of this wave see / any of them sees
@@ -494,59 +550,89 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs a, Cut cut, i
   f32x16 o[DT] = {};
   float m = -INFINITY, l = 0.0f;
 
+  // operand addresses of this lane: the permuted pieces differ per dimension step,
+  // everything else is an offset known when compiling
+  uint32_t ka[KS], va[DT];
+#pragma unroll
+  for (int i = 0; i < KS; ++i) ka[i] = key_at<D>(c, 2 * i + h);
+#pragma unroll
+  for (int d = 0; d < DT; ++d)  // keys 4 h + (lane & 15) / 4, dimensions 32 d + 16 (lane / 16 & 1) + 4 (lane & 3)
+    va[d] = 2 * kBuf + val_at<D>(4 * h + (lane & 15) / 4, 64 * d + 32 * ((lane >> 4) & 1) + 8 * (lane & 3));
   // staging: this thread's pieces are bytes [16 sp, 16 sp + 16) of keys sk + 64 / NP * i
   constexpr int TK = D / 16;  // threads of a key
   const int sk = threadIdx.x / TK, sp = threadIdx.x % TK;
+  const bool scaler = sp == 0 && sk % 16 == 0;  // also fetches its 16-key parts' scales
+  const int32_t* table = a.p.table + b * a.p.ld_table;
   u32x4 kr[NP], vr[NP];
-  float4 pr;
+  int32_t entry[NP];  // table entries of the pieces fetched next
+  float ksr[NP], vsr[NP];
+  int32_t pgr[NP];
+  // (positions past the end look up the last page: every load is of a page of the table)
+  auto look_up = [&](int32_t k0) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int32_t j = k0 + sk + (kBK / NP) * i;
+      entry[i] = table[(j < part.hi ? j : part.hi - 1) >> shift];
+    }
+  };
   auto fetch = [&](int32_t k0) {
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      const int32_t j = k0 + sk + (kBK / NP) * i, lp = j / page;
-      const int32_t pg = j < part.hi ? page_of(a.p, b, lp) : -1;
-      const bool held = pg >= 0 && j >= any_lo;
-      const int64_t at = ((int64_t(pg < 0 ? 0 : pg) * heads + head) * page + (j - lp * page)) * D + 16 * sp;
+      const int32_t j = k0 + sk + (kBK / NP) * i;
+      const bool there = j < part.hi && entry[i] >= 0 && entry[i] < a.p.pages;
+      pgr[i] = there ? entry[i] : -1;
+      const int64_t ph = int64_t(there ? entry[i] : 0) * heads + head;
+      const int64_t at = ((ph << shift) + (j & (page - 1))) * D + 16 * sp;
       kr[i] = *reinterpret_cast<const u32x4*>(a.kc + at);
       vr[i] = *reinterpret_cast<const u32x4*>(a.vc + at);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) vr[i][e] = held ? vr[i][e] : 0u;  // what no row sees counts for nothing
-    }
-    if (threadIdx.x < 4) {
-      const int32_t j = k0 + 16 * threadIdx.x;
-      const int32_t pg = j < part.hi ? page_of(a.p, b, j / page) : -1;
-      const int64_t at = int64_t(pg < 0 ? 0 : pg) * heads + head;
-      const PartScale ps = part_scale(pg, a.ks[at], a.vs[at], sm);
-      pr = make_float4(ps.c, ps.lv, ps.inv, static_cast<float>(ps.kind));
+      if (scaler) {
+        ksr[i] = a.ks[ph];
+        vsr[i] = a.vs[ph];
+      }
     }
   };
   auto stage = [&](int buf, int index) {
     uint32_t odd = 0;
+    uint8_t* kb = sh + buf * kBuf;
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       const int key = sk + (kBK / NP) * i;
-      *reinterpret_cast<u32x4*>(sh_k[buf] + key_at<D>(key, 2 * sp)) = bf16_of<F>(kr[i][0], kr[i][1]);
-      *reinterpret_cast<u32x4*>(sh_k[buf] + key_at<D>(key, 2 * sp + 1)) = bf16_of<F>(kr[i][2], kr[i][3]);
-      u32x4* v = reinterpret_cast<u32x4*>(sh_v[buf] + val_at<D>(key, 32 * sp));
+      const bool held = pgr[i] >= 0 && part.lo + kBK * index + key >= any_lo;
+      *reinterpret_cast<u32x4*>(kb + key_at<D>(key, 2 * sp)) = bf16_of<F>(kr[i][0], kr[i][1]);
+      *reinterpret_cast<u32x4*>(kb + key_at<D>(key, 2 * sp + 1)) = bf16_of<F>(kr[i][2], kr[i][3]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        vr[i][e] = held ? vr[i][e] : 0u;  // what no row sees counts for nothing
+        odd |= non_finite<F>(vr[i][e]);
+      }
+      u32x4* v = reinterpret_cast<u32x4*>(kb + 2 * kBuf + val_at<D>(key, 32 * sp));
       v[0] = f16_of<F>(vr[i][0], vr[i][1]);
       v[1] = f16_of<F>(vr[i][2], vr[i][3]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) odd |= non_finite<F>(vr[i][e]);
+      if (scaler) {
+        const PartScale ps = part_scale(pgr[i], ksr[i], vsr[i], sm);
+        sh_p[buf][key / 16] = make_float4(ps.c, ps.lv, ps.inv, static_cast<float>(ps.kind));
+      }
     }
     if (odd) sh_odd[buf] = index;
-    if (threadIdx.x < 4) sh_p[buf][threadIdx.x] = pr;
   };
   const int32_t steps = (part.hi - part.lo + kBK - 1) / kBK;
   if (threadIdx.x < 2) sh_odd[threadIdx.x] = -1;
   __syncthreads();
+  bool redo = false;
   if (steps > 0) {
+    look_up(part.lo);
     fetch(part.lo);
+    look_up(part.lo + kBK);
     stage(0, 0);
   }
   __syncthreads();
   for (int32_t t = 0; t < steps; ++t) {
     const int buf = t & 1;
     const int32_t k0 = part.lo + kBK * t;
-    if (t + 1 < steps) fetch(k0 + kBK);
+    if (t + 1 < steps) {
+      fetch(k0 + kBK);
+      look_up(k0 + 2 * kBK);
+    }
     if (k0 < w_any.hi && k0 + kBK > w_any.lo) {
       f32x16 z[2];
 #pragma unroll
@@ -555,7 +641,7 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs a, Cut cut, i
 #pragma unroll
         for (int i = 0; i < KS; ++i)
           z[kt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-              *reinterpret_cast<const bf16x8*>(sh_k[buf] + key_at<D>(32 * kt + c, 2 * i + h)),
+              *reinterpret_cast<const bf16x8*>(sh + (ka[i] + buf * kBuf) + 32 * kt * (2 * D)),
               __builtin_bit_cast(bf16x8, q[i]), z[kt], 0, 0, 0);
       }
       float4 ps[4];
@@ -600,11 +686,11 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs a, Cut cut, i
       f16x8 pf[4];  // weights of the tile's 16-key parts
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float shift = ps[e].y - base;
+        const float lift = ps[e].y - base;
         float w[8];
         float sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = exp2_fast(fmaf(z[e / 2][8 * (e % 2) + i], ps[e].x, shift));
+        for (int i = 0; i < 8; ++i) w[i] = exp2_fast(fmaf(z[e / 2][8 * (e % 2) + i], ps[e].x, lift));
         if (edge) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) w[i] = seen[e / 2] >> (8 * (e % 2) + i) & 1 ? w[i] : 0.0f;
@@ -617,43 +703,31 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs a, Cut cut, i
       }
       // values of part e, output tile d: keys 16 e + {0..3, 8..11} + 4 h, dimension 32 d + c
       auto values = [&](int e, int d) {
-        const int key = 16 * e + 4 * h + (lane & 15) / 4, byte = 64 * d + 32 * ((lane >> 4) & 1) + 8 * (lane & 3);
-        const u32x2 lo = read_tr(sh_v[buf] + val_at<D>(key, byte)), hi = read_tr(sh_v[buf] + val_at<D>(key + 8, byte));
+        const uint8_t* v = sh + (va[d] + buf * kBuf);
+        const u32x2 lo = read_tr(v + 16 * e * (2 * D)), hi = read_tr(v + (16 * e + 8) * (2 * D));
         return u32x4{lo[0], lo[1], hi[0], hi[1]};
       };
-      if (!(edge && sh_odd[buf] == t) && kind_hi <= kFine) {
+      redo = redo || (edge && sh_odd[buf] == t) || kind_hi > kFine;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+      for (int e = 0; e < 4; ++e)
 #pragma unroll
-          for (int d = 0; d < DT; ++d)
-            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, values(e, d)), pf[e], o[d], 0, 0, 0);
-      } else {
-        // key by key, each row taking the sum only if it sees the key
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          for (int key = 0; key < 16; ++key) {
-            const int kh = (key >> 2) & 1, slot = (key >> 3) * 4 + (key & 3);  // lane half and slot that hold it
-            const int32_t j = k0 + 16 * e + key;
-            const bool mine = j >= see.lo && j < see.hi && j < part.hi && ps[e].w != kAbsent;
-#pragma unroll
-            for (int d = 0; d < DT; ++d) {
-              u32x4 v = values(e, d);
-#pragma unroll
-              for (int p = 0; p < 4; ++p) {
-                if (ps[e].w > kFine) v[p] = blown_up(v[p], static_cast<int>(ps[e].w));
-                v[p] = h == kh && slot / 2 == p ? v[p] & (slot & 1 ? 0xFFFF0000u : 0x0000FFFFu) : 0u;
-              }
-              const f32x16 sum =
-                  __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, v), pf[e], o[d], 0, 0, 0);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[d][i] = mine ? sum[i] : o[d][i];
-            }
-          }
-        }
-      }
+        for (int d = 0; d < DT; ++d)
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, values(e, d)), pf[e], o[d], 0, 0, 0);
     }
     if (t + 1 < steps) stage(buf ^ 1, t + 1);
     __syncthreads();
+  }
+  if (redo) {
+    for (int row = 0; row < wr; ++row) {
+      const int32_t rr = r0 + 32 * wave + row;
+      const int64_t ti = s.tok0 + rr / group, hi = int64_t(head) * group + rr % group;
+      Range v = visible(a, s, rr / group);
+      v = Range{v.lo > part.lo ? v.lo : part.lo, v.hi < part.hi ? v.hi : part.hi};
+      float rm, rl, y[D / 64];
+      careful_row<F, D>(a, b, head, ti, hi, v, rm, rl, y);
+      careful_store<D>(a, parts, cut.chunks, chunk, ti, hi, rm, rl, y);
+    }
+    return;
   }
   l += __shfl_xor(l, 32);
   if (c >= wr) return;
