@@ -118,11 +118,11 @@ def lib():
         L.fp8_rmsnorm_backward.argtypes = [P, C.c_int, I64, I64, I64, P, C.c_int, I64, P, C.c_int, P, P, I64, P,
                                            I64, P, P]
         L.fp8_kv_append.restype = C.c_int
-        L.fp8_kv_append.argtypes = [P, P, C.c_int, I64, I64, I64, I64, I64, P, P, I64, I64, P, I64, C.c_int, F, I32,
+        L.fp8_kv_append.argtypes = [P, P, C.c_int, I64, I64, I64, I64, I64, P, P, I64, I64, P, I64, I64, C.c_int, F, I32,
                                     P, P, P, P, I64, I64, I64, I64, P]
         L.fp8_paged_attention.restype = C.c_int
         L.fp8_paged_attention.argtypes = [P, C.c_int, I64, I64, I64, I64, P, P, P, P, C.c_int, I64, I64, I64, I64, P,
-                                          I64, P, P, I64, I64, I64, F, I32, I64, P, C.c_int, I64, I64, P, P]
+                                          I64, I64, P, P, I64, I64, I64, F, I32, I64, P, C.c_int, I64, I64, P, P]
         _lib = L
     return _lib
 
@@ -138,22 +138,24 @@ def _ptr(t):
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream):
     if stream is not None:
         return stream.cuda_stream
     if _raw_stream is not None:  # the current stream's handle, without a Stream object
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(_device())
     return torch.cuda.current_stream().cuda_stream
 
 
 def _dtype(t: torch.Tensor) -> int:
-    if t.dtype == torch.float32:
-        return F32
-    if t.dtype == torch.bfloat16:
+    d = t.dtype
+    if d is torch.bfloat16:
         return BF16
-    raise TypeError("expected float32 or bfloat16, got %s" % t.dtype)
+    if d is torch.float32:
+        return F32
+    raise TypeError("expected float32 or bfloat16, got %s" % d)
 
 
 def _mat(t: torch.Tensor):
@@ -396,119 +398,115 @@ def fp8_weight_only_gemm(x, w, fw, gw, scale_w, y, bias=None, flags=0, stream=No
                                       _stream(stream)))
 
 
+# The checks of the functions below read each tensor attribute once: at a
+# decode step's sizes the calls are bound by this side, not by the GPU.
+
+def _rows(name, t, shape, dtype=None):
+    """Leading dimension of a row-major matrix of this shape (and type)."""
+    st = t.stride()
+    if t.shape != shape or st[1] != 1 or (dtype is not None and t.dtype is not dtype):
+        raise ValueError("%s must be row-major [%d x %d]%s" % (name, *shape, "" if dtype is None else " %s" % dtype))
+    return st[0]
+
+
+def _vec(name, t, n, dtype=None):
+    if t.shape != (n,) or not t.is_contiguous() or (dtype is not None and t.dtype is not dtype):
+        raise ValueError("%s must be a contiguous vector of %d%s" % (name, n, "" if dtype is None else " %s" % dtype))
+    return t.data_ptr()
+
+
+def _per_group(name, t, n):
+    if t.dtype is not torch.float32 or t.numel() < n or not t.is_contiguous():
+        raise ValueError("%s must be contiguous float32 with one entry per group" % name)
+    return t.data_ptr()
+
+
 def fp8_rmsnorm_quantize(x, weight, norm_eps, gran, fmt, mode, eps, pow2_round_up, scale, q, residual=None,
                          h=None, rstd=None, inv_scale=None, amax_out=None, stream=None):
     """Codes q and scales of RMSnorm(x + residual) * weight; h receives x + residual
     (rounded to x's type), rstd [rows] the norm's factors for the gradient."""
     rows, cols, ld = _mat(x)
-    qr, qc, ldq = _mat(q)
-    if (qr, qc) != (rows, cols) or q.dtype != torch.uint8:
-        raise ValueError("q must be uint8 [rows x cols]")
-    xt, ldr, ldh = _dtype(x), 0, 0
-    if residual is not None:
-        ldr = _like("residual", residual, rows, cols, x.dtype)
-    if h is not None:
-        ldh = _like("h", h, rows, cols, x.dtype)
-    _vec("weight", weight, cols)
-    if rstd is not None:
-        _vec("rstd", rstd, rows, torch.float32)
-    ns = ngroups(rows, gran[0]) * ngroups(cols, gran[1])
-    for name, t in (("scale", scale), ("inv_scale", inv_scale), ("amax_out", amax_out)):
-        if t is not None and (t.dtype != torch.float32 or t.numel() < ns or not t.is_contiguous()):
-            raise ValueError("%s must be contiguous float32 with one entry per group" % name)
-    _check("fp8_rmsnorm_quantize",
-           lib().fp8_rmsnorm_quantize(_ptr(x), xt, rows, cols, ld, _ptr(residual), ldr, _ptr(weight), _dtype(weight),
-                                      norm_eps, Gran(*gran), fmt, mode, eps, int(pow2_round_up), _ptr(scale),
-                                      _ptr(inv_scale), _ptr(q), ldq, _ptr(h), ldh, _ptr(rstd), _ptr(amax_out),
-                                      _stream(stream)))
+    shape, dtype = (rows, cols), x.dtype
+    gr, gc = gran
+    n = ngroups(rows, gr) * ngroups(cols, gc)
+    st = lib().fp8_rmsnorm_quantize(
+        x.data_ptr(), _dtype(x), rows, cols, ld, _ptr(residual),
+        0 if residual is None else _rows("residual", residual, shape, dtype), _vec("weight", weight, cols),
+        _dtype(weight), norm_eps, Gran(gr, gc), fmt, mode, eps, pow2_round_up, _per_group("scale", scale, n),
+        None if inv_scale is None else _per_group("inv_scale", inv_scale, n), q.data_ptr(),
+        _rows("q", q, shape, torch.uint8), _ptr(h), 0 if h is None else _rows("h", h, shape, dtype),
+        None if rstd is None else _vec("rstd", rstd, rows, torch.float32),
+        None if amax_out is None else _per_group("amax_out", amax_out, n), _stream(stream))
+    if st:
+        _check("fp8_rmsnorm_quantize", st)
 
 
 def fp8_rmsnorm_backward(dy, h, weight, rstd, dx, dweight=None, dresidual=None, stream=None):
     """dx (the gradient of h = x + residual, dresidual added) and dweight of
     fp8_rmsnorm_quantize, the cast taken as the identity."""
     rows, cols, lddy = _mat(dy)
-    ldh = _like("h", h, rows, cols)
-    lddx = _like("dx", dx, rows, cols, dy.dtype)
-    lddr = _like("dresidual", dresidual, rows, cols, dy.dtype) if dresidual is not None else 0
-    _vec("weight", weight, cols)
-    _vec("rstd", rstd, rows, torch.float32)
-    if dweight is not None:
-        _vec("dweight", dweight, cols, torch.float32)
-    _check("fp8_rmsnorm_backward",
-           lib().fp8_rmsnorm_backward(_ptr(dy), _dtype(dy), rows, cols, lddy, _ptr(h), _dtype(h), ldh, _ptr(weight),
-                                      _dtype(weight), _ptr(rstd), _ptr(dresidual), lddr, _ptr(dx), lddx,
-                                      _ptr(dweight), _stream(stream)))
-
-
-def _like(name, t, rows, cols, dtype=None):
-    r, c, ld = _mat(t)
-    if (r, c) != (rows, cols) or (dtype is not None and t.dtype != dtype):
-        raise ValueError("%s must be [%d x %d]%s" % (name, rows, cols, "" if dtype is None else " %s" % dtype))
-    return ld
-
-
-def _vec(name, t, n, dtype=None):
-    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous() or (dtype is not None and t.dtype != dtype):
-        raise ValueError("%s must be a contiguous vector of %d%s" % (name, n, "" if dtype is None else " %s" % dtype))
-
-
-def _heads(name, t, heads=None, dim=None):
-    """(tokens, heads, dim, token stride, head stride) of [tokens x heads x dim] with unit last stride."""
-    if t.dim() != 3 or t.stride(2) != 1 or (heads, dim) not in ((None, None), t.shape[1:]):
-        raise ValueError("%s must be [tokens x heads x head_dim] with unit last stride%s" % (
-            name, "" if heads is None else ", %d heads of %d" % (heads, dim)))
-    return t.shape[0], t.shape[1], t.shape[2], t.stride(0), t.stride(1)
+    shape, dtype = (rows, cols), dy.dtype
+    st = lib().fp8_rmsnorm_backward(
+        dy.data_ptr(), _dtype(dy), rows, cols, lddy, h.data_ptr(), _dtype(h), _rows("h", h, shape),
+        _vec("weight", weight, cols), _dtype(weight), _vec("rstd", rstd, rows, torch.float32), _ptr(dresidual),
+        0 if dresidual is None else _rows("dresidual", dresidual, shape, dtype), dx.data_ptr(),
+        _rows("dx", dx, shape, dtype), None if dweight is None else _vec("dweight", dweight, cols, torch.float32),
+        _stream(stream))
+    if st:
+        _check("fp8_rmsnorm_backward", st)
 
 
 def _paged(k_cache, v_cache, k_scale, v_scale, block_table, seq_start, kv_len):
-    """(pages, heads, page_size, head_dim, ld_table, seqs) of a paged cache and a batch's plan."""
-    shape = k_cache.shape
-    if (len(shape) != 4 or v_cache.shape != shape or k_cache.dtype != torch.uint8 or v_cache.dtype != torch.uint8
+    """(cache shape, width and leading dimension of the table, sequences) of a paged cache and a batch's plan."""
+    shape, u8, f32, i32 = k_cache.shape, torch.uint8, torch.float32, torch.int32
+    if (len(shape) != 4 or v_cache.shape != shape or k_cache.dtype is not u8 or v_cache.dtype is not u8
             or not k_cache.is_contiguous() or not v_cache.is_contiguous()):
         raise ValueError("k_cache and v_cache must be contiguous uint8 [pages x heads x page_size x head_dim]")
-    for t in (k_scale, v_scale):
-        if t.dtype != torch.float32 or t.shape != shape[:2] or not t.is_contiguous():
-            raise ValueError("k_scale and v_scale must be contiguous float32 [pages x heads]")
-    seqs = kv_len.shape[0]
-    if (block_table.dtype != torch.int32 or seq_start.dtype != torch.int32 or kv_len.dtype != torch.int32
-            or block_table.dim() != 2 or block_table.shape[0] != seqs or seq_start.shape != (seqs + 1,)
-            or block_table.stride(1) != 1 or not seq_start.is_contiguous() or not kv_len.is_contiguous()):
+    if (k_scale.dtype is not f32 or v_scale.dtype is not f32 or k_scale.shape != shape[:2]
+            or v_scale.shape != k_scale.shape or not k_scale.is_contiguous() or not v_scale.is_contiguous()):
+        raise ValueError("k_scale and v_scale must be contiguous float32 [pages x heads]")
+    seqs, st, tab = kv_len.numel(), block_table.stride(), block_table.shape
+    if (block_table.dtype is not i32 or seq_start.dtype is not i32 or kv_len.dtype is not i32 or len(st) != 2
+            or st[1] != 1 or tab[0] != seqs or seq_start.numel() != seqs + 1
+            or not seq_start.is_contiguous() or not kv_len.is_contiguous()):
         raise ValueError("block_table [seqs x n], seq_start [seqs + 1] and kv_len [seqs] must be int32 rows")
-    return (*shape, block_table.stride(0), seqs)
+    return shape, tab[1], max(st[0], tab[1]) if seqs == 1 else st[0], seqs  # (one row: any stride)
 
 
 def fp8_kv_append(k, v, k_cache, v_cache, k_scale, v_scale, fmt, block_table, seq_start, kv_len, max_new, eps=1e-12,
                   pow2_round_up=False, stream=None):
     """Quantizes new keys and values [tokens x heads x head_dim] into a paged cache of FP8 codes
     [pages x heads x page_size x head_dim] with one scale per page and head."""
-    pages, heads, page, dim, ldt, seqs = _paged(k_cache, v_cache, k_scale, v_scale, block_table, seq_start, kv_len)
-    tokens, _, _, ldk, hdk = _heads("k", k, heads, dim)
-    tv, _, _, ldv, hdv = _heads("v", v, heads, dim)
-    if tv != tokens or v.dtype != k.dtype:
-        raise ValueError("k and v must have the same tokens and type")
-    _check("fp8_kv_append",
-           lib().fp8_kv_append(_ptr(k), _ptr(v), _dtype(k), tokens, ldk, hdk, ldv, hdv, _ptr(seq_start),
-                               _ptr(kv_len), seqs, max_new, _ptr(block_table), ldt, fmt, eps, int(pow2_round_up),
-                               _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), pages, heads, page, dim,
-                               _stream(stream)))
+    (pages, heads, page, dim), width, ldt, seqs = _paged(k_cache, v_cache, k_scale, v_scale, block_table, seq_start, kv_len)
+    shape, sk, sv = k.shape, k.stride(), v.stride()
+    if (shape[1:] != (heads, dim) or v.shape != shape or v.dtype is not k.dtype or sk[2] != 1 or sv[2] != 1):
+        raise ValueError("k and v must be [tokens x heads x head_dim] of one type with unit last stride")
+    st = lib().fp8_kv_append(k.data_ptr(), v.data_ptr(), _dtype(k), shape[0], sk[0], sk[1], sv[0], sv[1],
+                             seq_start.data_ptr(), kv_len.data_ptr(), seqs, max_new, block_table.data_ptr(), width, ldt, fmt,
+                             eps, pow2_round_up, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                             v_scale.data_ptr(), pages, heads, page, dim, _stream(stream))
+    if st:
+        _check("fp8_kv_append", st)
 
 
 def fp8_paged_attention(q, k_cache, v_cache, k_scale, v_scale, fmt, block_table, seq_start, kv_len, max_new, max_kv,
                         sm_scale, y, causal=True, window=0, lse=None, stream=None):
     """y = attention of the new tokens' queries q [tokens x q_heads x head_dim] (bf16) over the paged FP8
     cache; max_new and max_kv bound the new tokens and the length of one sequence."""
-    pages, heads, page, dim, ldt, seqs = _paged(k_cache, v_cache, k_scale, v_scale, block_table, seq_start, kv_len)
-    tokens, qh, qd, ldq, hdq = _heads("q", q)
-    ty, yh, yd, ldy, hdy = _heads("y", y)
-    if qd != dim or (ty, yh, yd) != (tokens, qh, qd):
-        raise ValueError("q and y must be [tokens x q_heads x head_dim]")
-    if lse is not None and (lse.shape != (tokens, qh) or lse.dtype != torch.float32 or not lse.is_contiguous()):
+    (pages, heads, page, dim), width, ldt, seqs = _paged(k_cache, v_cache, k_scale, v_scale, block_table, seq_start, kv_len)
+    tokens, qh, qd = shape = q.shape
+    sq, sy = q.stride(), y.stride()
+    if qd != dim or y.shape != shape or sq[2] != 1 or sy[2] != 1:
+        raise ValueError("q and y must be [tokens x q_heads x head_dim] with unit last stride")
+    if lse is not None and (lse.shape != (tokens, qh) or lse.dtype is not torch.float32 or not lse.is_contiguous()):
         raise ValueError("lse must be contiguous float32 [tokens x q_heads]")
-    _check("fp8_paged_attention",
-           lib().fp8_paged_attention(_ptr(q), _dtype(q), tokens, qh, ldq, hdq, _ptr(k_cache), _ptr(v_cache),
-                                     _ptr(k_scale), _ptr(v_scale), fmt, pages, heads, page, dim, _ptr(block_table),
-                                     ldt, _ptr(seq_start), _ptr(kv_len), seqs, max_new, max_kv, sm_scale,
-                                     int(causal), window, _ptr(y), _dtype(y), ldy, hdy, _ptr(lse), _stream(stream)))
+    st = lib().fp8_paged_attention(q.data_ptr(), _dtype(q), tokens, qh, sq[0], sq[1], k_cache.data_ptr(),
+                                   v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), fmt, pages, heads, page,
+                                   dim, block_table.data_ptr(), width, ldt, seq_start.data_ptr(), kv_len.data_ptr(), seqs,
+                                   max_new, max_kv, sm_scale, causal, window, y.data_ptr(), _dtype(y), sy[0], sy[1],
+                                   _ptr(lse), _stream(stream))
+    if st:
+        _check("fp8_paged_attention", st)
 
 
 __all__ = ["fp8_rmsnorm_quantize", "fp8_rmsnorm_backward", "fp8_kv_append", "fp8_paged_attention",

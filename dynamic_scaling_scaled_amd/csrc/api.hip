@@ -623,11 +623,11 @@ namespace {
 
 // The plan of a batch over a paged cache, shared by append and attention.
 fp8rt_status paged_setup(const int32_t* seq_start, const int32_t* kv_len, int64_t seqs, int64_t tokens,
-                         int64_t max_new, const int32_t* block_table, int64_t ld_table, int64_t pages, int64_t heads,
+                         int64_t max_new, const int32_t* block_table, int64_t table_pages, int64_t ld_table, int64_t pages, int64_t heads,
                          int64_t page_size, int64_t head_dim, fp8rt_format f, PagedArgs& p) {
   constexpr int64_t kMax = int64_t(1) << 31;
   if (!seq_start || !kv_len || !block_table || !valid_fmt(f)) return FP8RT_EINVAL;
-  if (seqs <= 0 || tokens <= 0 || max_new <= 0 || ld_table <= 0 || pages <= 0 || heads <= 0 || page_size <= 0 ||
+  if (seqs <= 0 || tokens <= 0 || max_new <= 0 || table_pages <= 0 || ld_table < table_pages || pages <= 0 || heads <= 0 || page_size <= 0 ||
       head_dim <= 0)
     return FP8RT_EINVAL;
   if (seqs >= kMax || tokens >= kMax || ld_table >= kMax || pages >= kMax || heads > 65535) return FP8RT_EINVAL;
@@ -642,6 +642,7 @@ fp8rt_status paged_setup(const int32_t* seq_start, const int32_t* kv_len, int64_
   p.tokens = tokens;
   p.max_new = std::min(max_new, tokens);
   p.table = block_table;
+  p.width = table_pages;
   p.ld_table = ld_table;
   p.pages = pages;
   p.heads = static_cast<int>(heads);
@@ -655,14 +656,14 @@ fp8rt_status paged_setup(const int32_t* seq_start, const int32_t* kv_len, int64_
 
 fp8rt_status fp8_kv_append(const void* k, const void* v, fp8rt_dtype xt, int64_t tokens, int64_t ldk, int64_t hdk,
                            int64_t ldv, int64_t hdv, const int32_t* seq_start, const int32_t* kv_len, int64_t seqs,
-                           int64_t max_new, const int32_t* block_table, int64_t ld_table, fp8rt_format f, float eps,
+                           int64_t max_new, const int32_t* block_table, int64_t table_pages, int64_t ld_table, fp8rt_format f, float eps,
                            int32_t pow2_round_up, uint8_t* k_cache, uint8_t* v_cache, float* k_scale,
                            float* v_scale, int64_t pages, int64_t heads, int64_t page_size, int64_t head_dim,
                            hipStream_t stream) {
   if (!k || !v || !k_cache || !v_cache || !k_scale || !v_scale || !valid_dtype(xt) || !valid_eps(eps))
     return FP8RT_EINVAL;
   AppendArgs a;
-  const fp8rt_status st = paged_setup(seq_start, kv_len, seqs, tokens, max_new, block_table, ld_table, pages, heads,
+  const fp8rt_status st = paged_setup(seq_start, kv_len, seqs, tokens, max_new, block_table, table_pages, ld_table, pages, heads,
                                       page_size, head_dim, f, a.p);
   if (st != FP8RT_OK) return st;
   if (ldk < 0 || hdk < 0 || ldv < 0 || hdv < 0) return FP8RT_EINVAL;
@@ -689,14 +690,14 @@ fp8rt_status fp8_kv_append(const void* k, const void* v, fp8rt_dtype xt, int64_t
 fp8rt_status fp8_paged_attention(const void* q, fp8rt_dtype qt, int64_t tokens, int64_t q_heads, int64_t ldq,
                                  int64_t hdq, const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale,
                                  const float* v_scale, fp8rt_format f, int64_t pages, int64_t heads,
-                                 int64_t page_size, int64_t head_dim, const int32_t* block_table, int64_t ld_table,
+                                 int64_t page_size, int64_t head_dim, const int32_t* block_table, int64_t table_pages, int64_t ld_table,
                                  const int32_t* seq_start, const int32_t* kv_len, int64_t seqs, int64_t max_new,
                                  int64_t max_kv, float sm_scale, int32_t causal, int64_t window, void* y,
                                  fp8rt_dtype yt, int64_t ldy, int64_t hdy, float* lse, hipStream_t stream) {
   if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !y || !valid_dtype(qt) || !valid_dtype(yt))
     return FP8RT_EINVAL;
   AttendArgs a;
-  const fp8rt_status st = paged_setup(seq_start, kv_len, seqs, tokens, max_new, block_table, ld_table, pages, heads,
+  const fp8rt_status st = paged_setup(seq_start, kv_len, seqs, tokens, max_new, block_table, table_pages, ld_table, pages, heads,
                                       page_size, head_dim, f, a.p);
   if (st != FP8RT_OK) return st;
   if (q_heads <= 0 || q_heads > 65535 || q_heads % heads != 0 || max_kv <= 0 || window < 0 || !isfinite(sm_scale))
@@ -717,7 +718,7 @@ fp8rt_status fp8_paged_attention(const void* q, fp8rt_dtype qt, int64_t tokens, 
   a.vc = v_cache;
   a.ks = k_scale;
   a.vs = v_scale;
-  a.max_kv = std::min(max_kv, ld_table * page_size);
+  a.max_kv = std::min(max_kv, table_pages * page_size);
   a.sm_scale = sm_scale;
   a.causal = causal != 0;
   a.window = window;

@@ -261,7 +261,7 @@ struct PagedArgs {
   const int32_t* kv_len = nullptr;
   int64_t seqs = 0, tokens = 0, max_new = 0;
   const int32_t* table = nullptr;
-  int64_t ld_table = 0;
+  int64_t width = 0, ld_table = 0;  // entries of a row, and from row to row
   int64_t pages = 0;
   int heads = 0, page = 0, dim = 0;
   int fmt = 0;

@@ -13,7 +13,7 @@ struct SeqSpan {
   int64_t tok0;   // its first new token
   int32_t n;      // new tokens taken (at most max_new)
   int64_t first;  // position of its first new token (negative: kv_len below the number of new tokens)
-  int64_t len;    // positions that exist: kv_len, at most ld_table pages, at least 0
+  int64_t len;    // positions that exist: kv_len, at most the table's pages, at least 0
 };
 
 __device__ __forceinline__ SeqSpan seq_span(const PagedArgs& p, int64_t b) {
@@ -26,7 +26,7 @@ __device__ __forceinline__ SeqSpan seq_span(const PagedArgs& p, int64_t b) {
   s.first = len - (t1 - t0);
   s.n = static_cast<int32_t>(t1 - t0 < p.max_new ? t1 - t0 : p.max_new);
   // positions stay 32-bit with room for a tile past the end
-  const int64_t cap = p.ld_table * p.page < 0x7FFF0000 ? p.ld_table * p.page : 0x7FFF0000;
+  const int64_t cap = p.width * p.page < 0x7FFF0000 ? p.width * p.page : 0x7FFF0000;
   s.len = len < 0 ? 0 : len < cap ? len : cap;
   return s;
 }

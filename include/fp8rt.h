@@ -498,7 +498,7 @@ fp8rt_status fp8_rmsnorm_backward(const void* dy, fp8rt_dtype dyt, int64_t rows,
  * page_size 16, 32, 64 or 128 tokens; head_dim 64 or 128; seqs * (max_new / 16 +
  * 2) <= 2^23 (else FP8RT_EUNSUPPORTED).  Position p of
  * sequence b lives in slot p % page_size of page block_table[b][p / page_size]
- * (int32, leading dimension ld_table >= 1 entries).
+ * (int32 [seqs][table_pages], leading dimension ld_table >= table_pages).
  * A batch of `seqs` sequences hands in `tokens` new tokens, packed:
  *   seq_start : int32 [seqs + 1], sequence b owns tokens seq_start[b] ..
  *               seq_start[b+1] - 1 (none is allowed)
@@ -506,9 +506,9 @@ fp8rt_status fp8_rmsnorm_backward(const void* dy, fp8rt_dtype dyt, int64_t rows,
  *               the new ones are its last seq_start[b+1] - seq_start[b] positions
  *   max_new   : a bound on the new tokens of one sequence (host)
  * These arrays live on the device and are not read by the host: the kernels
- * bound every index by tokens, pages, ld_table and max_new.  A table entry outside
+ * bound every index by tokens, pages, table_pages and max_new.  A table entry outside
  * [0, pages) stands for a page that is not there (nothing is written to it,
- * attention takes its positions as hidden); positions past ld_table *
+ * attention takes its positions as hidden); positions past table_pages *
  * page_size (or 2^31 - 2^16) and before 0 are dropped in the same way, and so are tokens past max_new.
  *
  * fp8_kv_append writes the new tokens' keys and values into the cache.  For
@@ -526,7 +526,7 @@ fp8rt_status fp8_rmsnorm_backward(const void* dy, fp8rt_dtype dyt, int64_t rows,
  * aligned. */
 fp8rt_status fp8_kv_append(const void* k, const void* v, fp8rt_dtype xt, int64_t tokens, int64_t ldk, int64_t hdk,
                            int64_t ldv, int64_t hdv, const int32_t* seq_start, const int32_t* kv_len, int64_t seqs,
-                           int64_t max_new, const int32_t* block_table, int64_t ld_table, fp8rt_format f, float eps,
+                           int64_t max_new, const int32_t* block_table, int64_t table_pages, int64_t ld_table, fp8rt_format f, float eps,
                            int32_t pow2_round_up, uint8_t* k_cache, uint8_t* v_cache, float* k_scale,
                            float* v_scale, int64_t pages, int64_t heads, int64_t page_size, int64_t head_dim,
                            hipStream_t stream);
@@ -557,7 +557,7 @@ fp8rt_status fp8_kv_append(const void* k, const void* v, fp8rt_dtype xt, int64_t
 fp8rt_status fp8_paged_attention(const void* q, fp8rt_dtype qt, int64_t tokens, int64_t q_heads, int64_t ldq,
                                  int64_t hdq, const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale,
                                  const float* v_scale, fp8rt_format f, int64_t pages, int64_t heads,
-                                 int64_t page_size, int64_t head_dim, const int32_t* block_table, int64_t ld_table,
+                                 int64_t page_size, int64_t head_dim, const int32_t* block_table, int64_t table_pages, int64_t ld_table,
                                  const int32_t* seq_start, const int32_t* kv_len, int64_t seqs, int64_t max_new,
                                  int64_t max_kv, float sm_scale, int32_t causal, int64_t window, void* y,
                                  fp8rt_dtype yt, int64_t ldy, int64_t hdy, float* lse, hipStream_t stream);

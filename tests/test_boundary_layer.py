@@ -76,11 +76,11 @@ def test_gradient_refusals(rt, kw, status):
     assert grad(rt, **kw) == getattr(rt, status)
 
 
-PLAN = dict(tokens=4, start=FAKE, kv=FAKE, seqs=2, max_new=2, table=FAKE, ldt=4, f=0, kc=FAKE, vc=FAKE, ks=FAKE,
+PLAN = dict(tokens=4, start=FAKE, kv=FAKE, seqs=2, max_new=2, table=FAKE, width=4, ldt=4, f=0, kc=FAKE, vc=FAKE, ks=FAKE,
             vs=FAKE, pages=8, heads=2, page=16, dim=64)
 PLAN_BAD = [
     (dict(tokens=0), "EINVAL"), (dict(start=None), "EINVAL"), (dict(kv=None), "EINVAL"), (dict(seqs=0), "EINVAL"),
-    (dict(max_new=0), "EINVAL"), (dict(table=None), "EINVAL"), (dict(ldt=0), "EINVAL"), (dict(f=5), "EINVAL"),
+    (dict(max_new=0), "EINVAL"), (dict(table=None), "EINVAL"), (dict(width=0), "EINVAL"), (dict(ldt=3), "EINVAL"), (dict(f=5), "EINVAL"),
     (dict(kc=None), "EINVAL"), (dict(vc=None), "EINVAL"), (dict(ks=None), "EINVAL"), (dict(vs=None), "EINVAL"),
     (dict(pages=0), "EINVAL"), (dict(heads=0), "EINVAL"), (dict(page=0), "EINVAL"), (dict(dim=-64), "EINVAL"),
     (dict(tokens=2 ** 31), "EINVAL"), (dict(pages=2 ** 31), "EINVAL"), (dict(seqs=2 ** 31), "EINVAL"),
@@ -97,7 +97,7 @@ def append(rt, **kw):
     a = dict(PLAN, k=FAKE, v=FAKE, xt=rt.BF16, ldk=128, hdk=64, ldv=128, hdv=64, eps=1e-12)
     a.update(kw)
     return rt.lib().fp8_kv_append(a["k"], a["v"], a["xt"], a["tokens"], a["ldk"], a["hdk"], a["ldv"], a["hdv"],
-                                  a["start"], a["kv"], a["seqs"], a["max_new"], a["table"], a["ldt"], a["f"],
+                                  a["start"], a["kv"], a["seqs"], a["max_new"], a["table"], a["width"], a["ldt"], a["f"],
                                   a["eps"], 0, a["kc"], a["vc"], a["ks"], a["vs"], a["pages"], a["heads"], a["page"],
                                   a["dim"], None)
 
@@ -117,7 +117,7 @@ def attend(rt, **kw):
     a.update(kw)
     return rt.lib().fp8_paged_attention(a["q"], a["qt"], a["tokens"], a["qh"], a["ldq"], a["hdq"], a["kc"], a["vc"],
                                         a["ks"], a["vs"], a["f"], a["pages"], a["heads"], a["page"], a["dim"],
-                                        a["table"], a["ldt"], a["start"], a["kv"], a["seqs"], a["max_new"],
+                                        a["table"], a["width"], a["ldt"], a["start"], a["kv"], a["seqs"], a["max_new"],
                                         a["max_kv"], a["sm"], a["causal"], a["window"], a["y"], a["yt"], a["ldy"],
                                         a["hdy"], a["lse"], None)
 
