@@ -3,10 +3,10 @@
 //
 // Mathematics.  With t_j = z_j log2(e) the scores of the visible positions and
 // v_j = s_j dec(code_j) their values (s_j the page's v scale), the weight
-//   w_j = 2^(t_j + log2 s_j - m),   m >= max_j (t_j + log2 s_j) - kSlack,
+//   w_j = 2^(t_j + log2 s_j - m),   m at most 15 below max_j (t_j + log2 s_j),
 // turns the output into  y = sum_j w_j dec(code_j) / sum_j (w_j / s_j):  the codes go
-// into the second matrix product as they are, the weights reach at most
-// 2^kSlack whatever the pages' scales, and the sums follow in one pass over the keys
+// into the second matrix product as they are, the weights stay within
+// fp16 whatever the pages' scales, and the sums follow in one pass over the keys
 // (when m moves, the sums so far are multiplied by 2^(m_old - m_new)).
 // m + log2 sum_j (w_j / s_j) is the log-sum-exp in base 2.
 //
@@ -44,10 +44,14 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-// The running maximum follows only when a row passes it by 2^8: weights stay
-// below fp16's largest value, and the sums are seldom rescaled.
-constexpr float kSlack = 8.0f;
-// Scales below the smallest normal count as that: log2 and 1 / s stay finite.
+// The reference m follows the running maximum only when weights grow too large for
+// fp16: when a lane's weights of one 16-key part add up to this.
+constexpr float kFull = 32768.0f;
+// Before a row has seen a key, m is this: any score then gives an infinite
+// weight, which makes m follow.
+constexpr float kNoKey = -1e30f;
+// Scales below the smallest normal count as that: log2 and 1 / s stay finite, and a score of -Inf
+// times the k scale stays -Inf.
 constexpr float kTinyScale = 0x1p-126f;
 
 // Two codes (a half of a dword) as two bf16 / fp16 values, exactly.
@@ -136,16 +140,16 @@ struct Parts {
 };
 
 // What one 16-key part of a step needs from its page: t = dot * c, log2 of the v scale, its inverse.
-// A v scale that is not finite counts as 1 here, and the rows are done again by careful_row.
-constexpr int kAbsent = 0, kFine = 1, kNotFinite = 2;
+// A page that is not there gives weights of 0 (its codes are staged as 0).  Scales that are not
+// finite count as 1 here; the rows are done again by careful_row.
 struct PartScale {
   float c, lv, inv;
-  int kind;
 };
-__device__ __forceinline__ PartScale part_scale(int32_t pg, float ks, float vs, float sm) {
-  const bool fine = vs <= 3.4028235e38f;
-  const float v = !fine ? 1.0f : vs < kTinyScale ? kTinyScale : vs;
-  return PartScale{ks * sm, log2_fast(v), 1.0f / v, pg < 0 ? kAbsent : fine ? kFine : kNotFinite};
+__device__ __forceinline__ bool finite_scales(float ks, float vs) { return ks <= 3.4028235e38f && vs <= 3.4028235e38f; }
+__device__ __forceinline__ PartScale part_scale(bool there, float ks, float vs, float sm) {
+  const bool fine = finite_scales(ks, vs);
+  const float c = fine ? ks * sm : 1.0f, v = fine && vs >= kTinyScale ? vs : fine ? kTinyScale : 1.0f;
+  return PartScale{c < kTinyScale ? kTinyScale : c, there ? log2_fast(v) : -INFINITY, there ? 1.0f / v : 0.0f};
 }
 
 // One query row over the keys [see.lo, see.hi), by one wave, without products that hidden keys take
@@ -161,7 +165,7 @@ __device__ void careful_row(const AttendArgs& a, int64_t b, int32_t head, int64_
   const int32_t page = a.p.page;
   const uint16_t* q = a.q + tok * a.ldq + qh * a.hdq;
   const float sm = a.sm_scale * kLog2e;
-  m = -INFINITY;
+  m = kNoKey;
   l = 0.0f;
   for (int e = 0; e < E; ++e) y[e] = 0.0f;
   for (int32_t j0 = see.lo; j0 < see.hi; j0 += 64) {
@@ -181,8 +185,8 @@ __device__ void careful_row(const AttendArgs& a, int64_t b, int32_t head, int64_
     }
     float top = t;
     for (int d = 32; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-    const float mn = fmaxf(m, top), ref = mn == -INFINITY ? 0.0f : mn;
-    const float fade = exp2_fast(m - ref), w = exp2_fast(t - ref);
+    const float mn = fmaxf(m, top);
+    const float fade = exp2_fast(m - mn), w = exp2_fast(t - mn);
     float sum = w;
     for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
     l = l * fade + sum;
@@ -242,7 +246,7 @@ __global__ void __launch_bounds__(64 * W, W == 4 ? 3 : 1)
   __shared__ __align__(16) float sh_o[W][16][LD];
   __shared__ float2 sh_ml[W][16];
   __shared__ int sh_redo[W];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
   const int32_t heads = a.p.heads, group = static_cast<int32_t>(a.q_heads / heads);
   int64_t blk = blockIdx.x;
@@ -265,7 +269,8 @@ __global__ void __launch_bounds__(64 * W, W == 4 ? 3 : 1)
   const int64_t tok = s.tok0 + r / group;
   const int64_t qh = int64_t(head) * group + r % group;
   Range see = visible(a, s, r / group);
-  if (c >= rows) see.hi = see.lo;
+  see.hi = see.hi < part.hi ? see.hi : part.hi;
+  if (c >= rows || see.hi < see.lo) see.hi = see.lo;
   // positions that every row sees, and that any row sees
   const Range first = visible(a, s, r0 / group), last = visible(a, s, (r0 + rows - 1) / group);
   const int32_t all_lo = last.lo, all_hi = first.hi, any_lo = first.lo;
@@ -282,7 +287,7 @@ __global__ void __launch_bounds__(64 * W, W == 4 ? 3 : 1)
       for (int i = 0; i < 4; ++i) q[2 * h + u][i] ^= flip;
     }
   f32x4 o[DT] = {};
-  float m = -INFINITY, l = 0.0f;
+  float m = kNoKey, l = 0.0f;
 
   struct Step {
     u32x4 k[2][KD];
@@ -335,60 +340,55 @@ __global__ void __launch_bounds__(64 * W, W == 4 ? 3 : 1)
           z[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
               __builtin_bit_cast(bf16x8, bf16_of<F>(cur.k[t][h][2 * u], cur.k[t][h][2 * u + 1])),
               __builtin_bit_cast(bf16x8, q[2 * h + u]), z[t], 0, 0, 0);
-      ps[t] = part_scale(cur.pg[t], cur.ks[t], cur.vs[t], sm);
+      ps[t] = part_scale(cur.pg[t] >= 0, cur.ks[t], cur.vs[t], sm);
+      redo |= cur.pg[t] >= 0 && !finite_scales(cur.ks[t], cur.vs[t]);
     }
-    const bool edge = k0 < all_lo || k0 + 32 > all_hi || k0 + 32 > part.hi || cur.pg[0] < 0 || cur.pg[1] < 0;
-    uint32_t seen = 0xFFu;  // bit 4 t + i: this lane's row sees key 16 t + 4 g + i
-    if (edge) {
-      seen = 0;
-      uint32_t held = 0;    // keys that some row sees
+    if (k0 < all_lo || k0 + 32 > all_hi || k0 + 32 > part.hi || cur.pg[0] < 0 || cur.pg[1] < 0) {
+      // hidden keys score -Inf; values that no row sees are 0, the rest must be finite
+      const int32_t from = see.lo - k0 - 4 * g;
+      const uint32_t n = see.hi - see.lo;
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int32_t j = k0 + 16 * t + 4 * g + i;
-          const bool there = cur.pg[t] >= 0 && j < part.hi;
-          if (there && j >= see.lo && j < see.hi) seen |= 1u << (4 * t + i);
-          if (there && j >= any_lo) held |= 1u << (4 * t + i);
-          if (!(seen >> (4 * t + i) & 1)) z[t][i] = -INFINITY;
-        }
+          const bool held = cur.pg[t] >= 0 && j >= any_lo && j < part.hi;
+          z[t][i] = held && static_cast<uint32_t>(16 * t + i - from) < n ? z[t][i] : -INFINITY;
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int w = 0; w < VW; ++w) {
-          if (!(held >> j & 1)) cur.v[j][w] = 0;
-          redo |= non_finite<F>(cur.v[j][w]);
+          for (int w = 0; w < VW; ++w) {
+            cur.v[4 * t + i][w] = held ? cur.v[4 * t + i][w] : 0u;
+            redo |= non_finite<F>(cur.v[4 * t + i][w]);
+          }
         }
     }
-    redo |= ps[0].kind == kNotFinite || ps[1].kind == kNotFinite;
-    float top = -INFINITY;
+    float w[8], sum[2];
+    auto weigh = [&] {
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
-      top = fmaxf(top, fmaf(fmaxf(fmaxf(z[t][0], z[t][1]), fmaxf(z[t][2], z[t][3])), ps[t].c, ps[t].lv));
-    if (__any(top > m + kSlack)) {
+      for (int t = 0; t < 2; ++t) {
+        const float lift = ps[t].lv - m;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[4 * t + i] = exp2_fast(fmaf(z[t][i], ps[t].c, lift));
+        sum[t] = (w[4 * t] + w[4 * t + 1]) + (w[4 * t + 2] + w[4 * t + 3]);
+      }
+    };
+    weigh();
+    if (__any(!(fmaxf(sum[0], sum[1]) < kFull))) {
+      float top = kNoKey;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        top = fmaxf(top, fmaf(fmaxf(fmaxf(z[t][0], z[t][1]), fmaxf(z[t][2], z[t][3])), ps[t].c, ps[t].lv));
       top = fmaxf(top, __shfl_xor(top, 16));
       top = fmaxf(top, __shfl_xor(top, 32));
       const float mn = fmaxf(m, top);
-      const float fade = mn == -INFINITY ? 1.0f : exp2_fast(m - mn);
+      const float fade = exp2_fast(m - mn);
       l *= fade;
 #pragma unroll
       for (int d = 0; d < DT; ++d) o[d] *= fade;
       m = mn;
+      weigh();
     }
-    const float base = m == -INFINITY ? 0.0f : m;
-    float w[8];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const float lift = ps[t].lv - base;
-      float sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float e = exp2_fast(fmaf(z[t][i], ps[t].c, lift));
-        w[4 * t + i] = seen >> (4 * t + i) & 1 ? e : 0.0f;
-        sum += w[4 * t + i];
-      }
-      l = fmaf(sum, ps[t].inv, l);
-    }
+    l = fmaf(sum[0], ps[0].inv, l);
+    l = fmaf(sum[1], ps[1].inv, l);
     const u32x4 pw = u32x4{pack_f16(w[0], w[1]), pack_f16(w[2], w[3]), pack_f16(w[4], w[5]), pack_f16(w[6], w[7])};
     const f16x8 pf = __builtin_bit_cast(f16x8, pw);
     // value operands of the 16-wide tiles of dword x: key pairs of each byte
@@ -443,10 +443,9 @@ __global__ void __launch_bounds__(64 * W, W == 4 ? 3 : 1)
   }
   for (int e = threadIdx.x; e < rows * (D / 4); e += 64 * W) {
     const int row = e / (D / 4), d = e % (D / 4) * 4;
-    float mt = -INFINITY;
+    float base = kNoKey;
 #pragma unroll
-    for (int w = 0; w < W; ++w) mt = fmaxf(mt, sh_ml[w][row].x);
-    const float base = mt == -INFINITY ? 0.0f : mt;
+    for (int w = 0; w < W; ++w) base = fmaxf(base, sh_ml[w][row].x);
     float lt = 0.0f;
     f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -466,7 +465,7 @@ __global__ void __launch_bounds__(64 * W, W == 4 ? 3 : 1)
     } else {
       const int64_t at = (int64_t(chunk) * a.p.tokens + t) * a.q_heads + h;
       *reinterpret_cast<f32x4*>(parts.o + at * D + d) = y;
-      if (d == 0) parts.ml[at] = make_float2(mt, lt);
+      if (d == 0) parts.ml[at] = make_float2(base, lt);
     }
   }
 }
@@ -504,9 +503,10 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs a, Cut cut, i
   constexpr int DT = D / 32;   // 32-wide output tiles
   constexpr int kBuf = kBK * D * 2;  // bytes of one buffer of keys, and of values
   __shared__ __align__(16) uint8_t sh[4 * kBuf];  // keys 0, keys 1, values 0, values 1
-  __shared__ __align__(16) float4 sh_p[2][4];  // PartScale of the tile's 16-key parts
-  __shared__ int sh_odd[2];                    // the last tile of this buffer with a value code that is not finite
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __shared__ __align__(16) float4 sh_p[2][4];     // PartScale of the tile's 16-key parts
+  __shared__ int sh_odd[2];                       // the last tile of this buffer with a value code that is not finite
+  __shared__ int sh_bad[2];                       // ... with a scale that is not finite
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 31, h = lane >> 5;
   const int32_t heads = a.p.heads, group = static_cast<int32_t>(a.q_heads / heads);
   int64_t blk = blockIdx.x;
@@ -524,11 +524,11 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs a, Cut cut, i
   const Range part = chunk_of(tile, cut, chunk);
   if (chunk > 0 && part.lo >= part.hi) return;
   const int32_t page = a.p.page, shift = 31 - __builtin_clz(page);
-  const int32_t any_lo = visible(a, s, r0 / group).lo;
-
-  // this lane's query row, and what all rows of this wave see / any of them sees
+  // positions that some row of the workgroup sees, that all of them see; the same for this wave
   const int32_t wr = rows - 32 * wave < 32 ? rows - 32 * wave : 32;  // rows of this wave (may be <= 0)
-  const int32_t r = r0 + 32 * wave + (c < wr ? c : 0);
+  const Range wg_first = visible(a, s, r0 / group), wg_last = visible(a, s, (r0 + rows - 1) / group);
+  const int32_t any_lo = wg_first.lo, all_lo = wg_last.lo, all_hi = wg_first.hi;
+  const int32_t r = r0 + 32 * wave + (c < wr ? c : 0);  // this lane's query row
   const int64_t tok = s.tok0 + (wr > 0 ? r / group : 0);
   const int64_t qh = int64_t(head) * group + r % group;
   Range see = {0, 0}, w_all = {0, 0}, w_any = {0, 0};
@@ -537,6 +537,9 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs a, Cut cut, i
     w_all = Range{e.lo, f.hi};
     w_any = Range{f.lo, e.hi};
     if (c < wr) see = visible(a, s, r / group);
+    if (wr < 32) w_all.hi = w_all.lo;  // idle rows see nothing: every tile is an edge
+    see.hi = see.hi < part.hi ? see.hi : part.hi;
+    see.hi = see.hi > see.lo ? see.hi : see.lo;
   }
   const float sm = fabsf(a.sm_scale) * kLog2e;
   const uint32_t flip = a.sm_scale < 0.0f ? 0x80008000u : 0u;
@@ -548,7 +551,7 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs a, Cut cut, i
     for (int j = 0; j < 4; ++j) q[i][j] ^= flip;
   }
   f32x16 o[DT] = {};
-  float m = -INFINITY, l = 0.0f;
+  float m = kNoKey, l = 0.0f;
 
   // operand addresses of this lane: the permuted pieces differ per dimension step,
   // everything else is an offset known when compiling
@@ -558,15 +561,18 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs a, Cut cut, i
 #pragma unroll
   for (int d = 0; d < DT; ++d)  // keys 4 h + (lane & 15) / 4, dimensions 32 d + 16 (lane / 16 & 1) + 4 (lane & 3)
     va[d] = 2 * kBuf + val_at<D>(4 * h + (lane & 15) / 4, 64 * d + 32 * ((lane >> 4) & 1) + 8 * (lane & 3));
+
   // staging: this thread's pieces are bytes [16 sp, 16 sp + 16) of keys sk + 64 / NP * i
   constexpr int TK = D / 16;  // threads of a key
   const int sk = threadIdx.x / TK, sp = threadIdx.x % TK;
   const bool scaler = sp == 0 && sk % 16 == 0;  // also fetches its 16-key parts' scales
   const int32_t* table = a.p.table + b * a.p.ld_table;
+  const uint32_t page_bytes = static_cast<uint32_t>(page) * D, pitch = page_bytes * heads;
+  const int64_t lane_at = int64_t(head) * page_bytes + 16 * sp;
   u32x4 kr[NP], vr[NP];
   int32_t entry[NP];  // table entries of the pieces fetched next
   float ksr[NP], vsr[NP];
-  int32_t pgr[NP];
+  bool there[NP];     // the page of the piece fetched last is present, and the position exists
   // (positions past the end look up the last page: every load is of a page of the table)
   auto look_up = [&](int32_t k0) {
 #pragma unroll
@@ -579,44 +585,54 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs a, Cut cut, i
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       const int32_t j = k0 + sk + (kBK / NP) * i;
-      const bool there = j < part.hi && entry[i] >= 0 && entry[i] < a.p.pages;
-      pgr[i] = there ? entry[i] : -1;
-      const int64_t ph = int64_t(there ? entry[i] : 0) * heads + head;
-      const int64_t at = ((ph << shift) + (j & (page - 1))) * D + 16 * sp;
+      there[i] = j < part.hi && static_cast<uint32_t>(entry[i]) < static_cast<uint32_t>(a.p.pages);
+      const uint32_t pg = there[i] ? entry[i] : 0;
+      const int64_t at = static_cast<int64_t>(static_cast<uint64_t>(pg) * pitch + (lane_at + (j & (page - 1)) * D));
       kr[i] = *reinterpret_cast<const u32x4*>(a.kc + at);
       vr[i] = *reinterpret_cast<const u32x4*>(a.vc + at);
       if (scaler) {
+        const int64_t ph = int64_t(pg) * heads + head;
         ksr[i] = a.ks[ph];
         vsr[i] = a.vs[ph];
       }
     }
   };
   auto stage = [&](int buf, int index) {
-    uint32_t odd = 0;
     uint8_t* kb = sh + buf * kBuf;
+    const int32_t k0 = part.lo + kBK * index;
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       const int key = sk + (kBK / NP) * i;
-      const bool held = pgr[i] >= 0 && part.lo + kBK * index + key >= any_lo;
+      if (__any(!there[i])) {  // what is not there has codes of 0
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          kr[i][e] = there[i] ? kr[i][e] : 0u;
+          vr[i][e] = there[i] ? vr[i][e] : 0u;
+        }
+      }
+      if (k0 < all_lo || k0 + kBK > all_hi) {  // hidden from some row: not finite counts
+        uint32_t odd = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          vr[i][e] = k0 + key >= any_lo ? vr[i][e] : 0u;
+          odd |= non_finite<F>(vr[i][e]);
+        }
+        if (odd) sh_odd[buf] = index;
+      }
       *reinterpret_cast<u32x4*>(kb + key_at<D>(key, 2 * sp)) = bf16_of<F>(kr[i][0], kr[i][1]);
       *reinterpret_cast<u32x4*>(kb + key_at<D>(key, 2 * sp + 1)) = bf16_of<F>(kr[i][2], kr[i][3]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        vr[i][e] = held ? vr[i][e] : 0u;  // what no row sees counts for nothing
-        odd |= non_finite<F>(vr[i][e]);
-      }
       u32x4* v = reinterpret_cast<u32x4*>(kb + 2 * kBuf + val_at<D>(key, 32 * sp));
       v[0] = f16_of<F>(vr[i][0], vr[i][1]);
       v[1] = f16_of<F>(vr[i][2], vr[i][3]);
       if (scaler) {
-        const PartScale ps = part_scale(pgr[i], ksr[i], vsr[i], sm);
-        sh_p[buf][key / 16] = make_float4(ps.c, ps.lv, ps.inv, static_cast<float>(ps.kind));
+        const PartScale ps = part_scale(there[i], ksr[i], vsr[i], sm);
+        sh_p[buf][key / 16] = make_float4(ps.c, ps.lv, ps.inv, 0.0f);
+        if (there[i] && !finite_scales(ksr[i], vsr[i])) sh_bad[buf] = index;
       }
     }
-    if (odd) sh_odd[buf] = index;
   };
   const int32_t steps = (part.hi - part.lo + kBK - 1) / kBK;
-  if (threadIdx.x < 2) sh_odd[threadIdx.x] = -1;
+  if (threadIdx.x < 2) sh_odd[threadIdx.x] = sh_bad[threadIdx.x] = -1;
   __syncthreads();
   bool redo = false;
   if (steps > 0) {
@@ -634,85 +650,83 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs a, Cut cut, i
       look_up(k0 + 2 * kBK);
     }
     if (k0 < w_any.hi && k0 + kBK > w_any.lo) {
-      f32x16 z[2];
+      const uint32_t at = buf * kBuf;
+      auto key_of = [&](int kt, int i) {
+        return *reinterpret_cast<const bf16x8*>(sh + (ka[i] + at) + 32 * kt * (2 * D));
+      };
+      f32x16 z[2] = {};
+      bf16x8 kf[KS];
 #pragma unroll
-      for (int kt = 0; kt < 2; ++kt) {
-        z[kt] = f32x16{};
+      for (int i = 0; i < KS; ++i) kf[i] = key_of(0, i);
 #pragma unroll
-        for (int i = 0; i < KS; ++i)
-          z[kt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-              *reinterpret_cast<const bf16x8*>(sh + (ka[i] + buf * kBuf) + 32 * kt * (2 * D)),
-              __builtin_bit_cast(bf16x8, q[i]), z[kt], 0, 0, 0);
+      for (int i = 0; i < KS; ++i) {
+        z[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[i], __builtin_bit_cast(bf16x8, q[i]), z[0], 0, 0, 0);
+        kf[i] = key_of(1, i);
       }
+#pragma unroll
+      for (int i = 0; i < KS; ++i)
+        z[1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[i], __builtin_bit_cast(bf16x8, q[i]), z[1], 0, 0, 0);
       float4 ps[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) ps[i] = sh_p[buf][i];
-      const float kind_lo = fminf(fminf(ps[0].w, ps[1].w), fminf(ps[2].w, ps[3].w));
-      const float kind_hi = fmaxf(fmaxf(ps[0].w, ps[1].w), fmaxf(ps[2].w, ps[3].w));
-      const bool edge = k0 < w_all.lo || k0 + kBK > w_all.hi || k0 + kBK > part.hi || kind_lo == kAbsent;
       // register 8 e + i of part 2 kt + e is key 32 kt + 16 e + 8 (i / 4) + 4 h + i % 4
-      uint32_t seen[2] = {0xFFFFu, 0xFFFFu};
+      const bool edge = k0 < w_all.lo || k0 + kBK > w_all.hi || k0 + kBK > part.hi;
+      redo = redo || sh_bad[buf] == t || (edge && sh_odd[buf] == t);
       if (edge) {
+        const int32_t from = see.lo - k0 - 4 * h;
+        const uint32_t n = see.hi - see.lo;
 #pragma unroll
-        for (int kt = 0; kt < 2; ++kt) {
-          seen[kt] = 0;
+        for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int32_t j = k0 + 32 * kt + 8 * (i / 4) + 4 * h + i % 4;
-            const bool v = j >= see.lo && j < see.hi && j < part.hi && ps[2 * kt + i / 8].w != kAbsent;
-            seen[kt] |= v ? 1u << i : 0u;
-            z[kt][i] = v ? z[kt][i] : -INFINITY;
-          }
+          for (int i = 0; i < 16; ++i)
+            z[kt][i] = static_cast<uint32_t>(32 * kt + 8 * (i / 4) + i % 4 - from) < n ? z[kt][i] : -INFINITY;
+      }
+      f16x8 pf[4];   // weights of the tile's 16-key parts
+      float sum[4];  // this lane's sums of them
+      auto weigh = [&] {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float lift = ps[e].y - m;
+          float w[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[i] = exp2_fast(fmaf(z[e / 2][8 * (e % 2) + i], ps[e].x, lift));
+          sum[e] = ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
+          pf[e] = __builtin_bit_cast(f16x8, (u32x4{pack_f16(w[0], w[1]), pack_f16(w[2], w[3]), pack_f16(w[4], w[5]),
+                                                   pack_f16(w[6], w[7])}));
         }
-      }
-      float top = -INFINITY;
+      };
+      weigh();
+      if (__any(!(fmaxf(fmaxf(sum[0], sum[1]), fmaxf(sum[2], sum[3])) < kFull))) {
+        float top = kNoKey;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float x = -INFINITY;
+        for (int e = 0; e < 4; ++e) {
+          float x = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x = fmaxf(x, z[e / 2][8 * (e % 2) + i]);
-        top = fmaxf(top, fmaf(x, ps[e].x, ps[e].y));
-      }
-      if (__any(top > m + kSlack)) {
+          for (int i = 0; i < 8; ++i) x = fmaxf(x, z[e / 2][8 * (e % 2) + i]);
+          top = fmaxf(top, fmaf(x, ps[e].x, ps[e].y));
+        }
         top = fmaxf(top, __shfl_xor(top, 32));
         const float mn = fmaxf(m, top);
-        const float fade = mn == -INFINITY ? 1.0f : exp2_fast(m - mn);
+        const float fade = exp2_fast(m - mn);
         l *= fade;
 #pragma unroll
         for (int d = 0; d < DT; ++d) o[d] *= fade;
         m = mn;
+        weigh();
       }
-      const float base = m == -INFINITY ? 0.0f : m;
-      f16x8 pf[4];  // weights of the tile's 16-key parts
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float lift = ps[e].y - base;
-        float w[8];
-        float sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = exp2_fast(fmaf(z[e / 2][8 * (e % 2) + i], ps[e].x, lift));
-        if (edge) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) w[i] = seen[e / 2] >> (8 * (e % 2) + i) & 1 ? w[i] : 0.0f;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum += w[i];
-        l = fmaf(sum, ps[e].z, l);
-        pf[e] = __builtin_bit_cast(f16x8, (u32x4{pack_f16(w[0], w[1]), pack_f16(w[2], w[3]), pack_f16(w[4], w[5]),
-                                                 pack_f16(w[6], w[7])}));
-      }
+      for (int e = 0; e < 4; ++e) l = fmaf(sum[e], ps[e].z, l);
       // values of part e, output tile d: keys 16 e + {0..3, 8..11} + 4 h, dimension 32 d + c
-      auto values = [&](int e, int d) {
-        const uint8_t* v = sh + (va[d] + buf * kBuf);
+      auto value_of = [&](int e, int d) {
+        const uint8_t* v = sh + (va[d] + at);
         const u32x2 lo = read_tr(v + 16 * e * (2 * D)), hi = read_tr(v + (16 * e + 8) * (2 * D));
-        return u32x4{lo[0], lo[1], hi[0], hi[1]};
+        return __builtin_bit_cast(f16x8, (u32x4{lo[0], lo[1], hi[0], hi[1]}));
       };
-      redo = redo || (edge && sh_odd[buf] == t) || kind_hi > kFine;
 #pragma unroll
       for (int e = 0; e < 4; ++e)
 #pragma unroll
         for (int d = 0; d < DT; ++d)
-          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, values(e, d)), pf[e], o[d], 0, 0, 0);
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(value_of(e, d), pf[e], o[d], 0, 0, 0);
     }
     if (t + 1 < steps) stage(buf ^ 1, t + 1);
     __syncthreads();
@@ -772,11 +786,10 @@ __global__ void __launch_bounds__(256) k_attend_join(AttendArgs a, Cut cut, int3
   int64_t n = (int64_t(tile.hi) - tile.lo + cut.len - 1) / cut.len;
   n = n < 1 ? 1 : n > cut.chunks ? cut.chunks : n;
   const int64_t tok = s.tok0 + i, row = tok * a.q_heads + h, step = a.p.tokens * a.q_heads;
-  float top = -INFINITY;
-  for (int64_t k = lane; k < n; k += 64) top = fmaxf(top, parts.ml[k * step + row].x);
+  float base = kNoKey;
+  for (int64_t k = lane; k < n; k += 64) base = fmaxf(base, parts.ml[k * step + row].x);
 #pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-  const float base = top == -INFINITY ? 0.0f : top;
+  for (int d = 32; d >= 1; d >>= 1) base = fmaxf(base, __shfl_xor(base, d));
   float l = 0.0f, y[E] = {};
 #pragma unroll 4
   for (int64_t k = 0; k < n; ++k) {
