@@ -94,6 +94,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   v[1] = static_cast<__bf16>(b);
   return __builtin_bit_cast(uint32_t, v);
 }
+// A value that every lane has, in a scalar register.
+__device__ __forceinline__ float uniform(float x) {
+  return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(x)));
+}
+// Keeps the compiler from moving instructions across this point: the kernels' loops
+// say themselves which work runs under which matrix instruction.
+__device__ __forceinline__ void pin() { __builtin_amdgcn_sched_barrier(0); }
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float log2_fast(float x) { return __builtin_amdgcn_logf(x); }
 
@@ -149,7 +156,8 @@ __device__ __forceinline__ bool finite_scales(float ks, float vs) { return ks <=
 __device__ __forceinline__ PartScale part_scale(bool there, float ks, float vs, float sm) {
   const bool fine = finite_scales(ks, vs);
   const float c = fine ? ks * sm : 1.0f, v = fine && vs >= kTinyScale ? vs : fine ? kTinyScale : 1.0f;
-  return PartScale{c < kTinyScale ? kTinyScale : c, there ? log2_fast(v) : -INFINITY, there ? 1.0f / v : 0.0f};
+  return PartScale{c < kTinyScale ? kTinyScale : c, there ? log2_fast(v) : -INFINITY,
+                   there ? __builtin_amdgcn_rcpf(v) : 0.0f};  // (rcp: 1 ulp)
 }
 
 // One query row over the keys [see.lo, see.hi), by one wave, without products that hidden keys take
@@ -503,9 +511,8 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs a, Cut cut, i
   constexpr int DT = D / 32;   // 32-wide output tiles
   constexpr int kBuf = kBK * D * 2;  // bytes of one buffer of keys, and of values
   __shared__ __align__(16) uint8_t sh[4 * kBuf];  // keys 0, keys 1, values 0, values 1
-  __shared__ __align__(16) float4 sh_p[2][4];     // PartScale of the tile's 16-key parts
+  __shared__ __align__(16) float4 sh_p[2][4];     // PartScale of the tile's 16-key parts; scales not finite
   __shared__ int sh_odd[2];                       // the last tile of this buffer with a value code that is not finite
-  __shared__ int sh_bad[2];                       // ... with a scale that is not finite
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 31, h = lane >> 5;
   const int32_t heads = a.p.heads, group = static_cast<int32_t>(a.q_heads / heads);
@@ -565,14 +572,20 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs a, Cut cut, i
   // staging: this thread's pieces are bytes [16 sp, 16 sp + 16) of keys sk + 64 / NP * i
   constexpr int TK = D / 16;  // threads of a key
   const int sk = threadIdx.x / TK, sp = threadIdx.x % TK;
-  const bool scaler = sp == 0 && sk % 16 == 0;  // also fetches its 16-key parts' scales
   const int32_t* table = a.p.table + b * a.p.ld_table;
   const uint32_t page_bytes = static_cast<uint32_t>(page) * D, pitch = page_bytes * heads;
-  const int64_t lane_at = int64_t(head) * page_bytes + 16 * sp;
+  const uint32_t pages = static_cast<uint32_t>(a.p.pages);
+  uint64_t lane_at[NP];  // the piece's place in its page (a tile starts at a multiple of 64)
+#pragma unroll
+  for (int i = 0; i < NP; ++i)
+    lane_at[i] = uint64_t(head) * page_bytes + ((sk + (kBK / NP) * i) & (page - 1)) * D + 16 * sp;
   u32x4 kr[NP], vr[NP];
-  int32_t entry[NP];  // table entries of the pieces fetched next
-  float ksr[NP], vsr[NP];
-  bool there[NP];     // the page of the piece fetched last is present, and the position exists
+  int32_t entry[NP];   // table entries of the pieces fetched next
+  bool there[NP];      // the page of the piece fetched last is present, and the position exists
+  // This wave looks after the scales of the tile's 16-key part number `wave`, in scalars.
+  int32_t part_entry;
+  float ksr, vsr;
+  bool part_there;
   // (positions past the end look up the last page: every load is of a page of the table)
   auto look_up = [&](int32_t k0) {
 #pragma unroll
@@ -580,37 +593,38 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs a, Cut cut, i
       const int32_t j = k0 + sk + (kBK / NP) * i;
       entry[i] = table[(j < part.hi ? j : part.hi - 1) >> shift];
     }
+    const int32_t j = k0 + 16 * wave;
+    part_entry = table[(j < part.hi ? j : part.hi - 1) >> shift];
   };
   auto fetch = [&](int32_t k0) {
+    const int32_t inside = (k0 & (page - 1) & kBK) * D;  // pages of 128: their second half
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      const int32_t j = k0 + sk + (kBK / NP) * i;
-      there[i] = j < part.hi && static_cast<uint32_t>(entry[i]) < static_cast<uint32_t>(a.p.pages);
-      const uint32_t pg = there[i] ? entry[i] : 0;
-      const int64_t at = static_cast<int64_t>(static_cast<uint64_t>(pg) * pitch + (lane_at + (j & (page - 1)) * D));
-      kr[i] = *reinterpret_cast<const u32x4*>(a.kc + at);
-      vr[i] = *reinterpret_cast<const u32x4*>(a.vc + at);
-      if (scaler) {
-        const int64_t ph = int64_t(pg) * heads + head;
-        ksr[i] = a.ks[ph];
-        vsr[i] = a.vs[ph];
-      }
+      there[i] = k0 + sk + (kBK / NP) * i < part.hi && static_cast<uint32_t>(entry[i]) < pages;
+      const uint64_t at = uint64_t(there[i] ? static_cast<uint32_t>(entry[i]) : 0u) * pitch + lane_at[i];
+      kr[i] = *reinterpret_cast<const u32x4*>(a.kc + inside + at);
+      vr[i] = *reinterpret_cast<const u32x4*>(a.vc + inside + at);
     }
+    part_there = k0 + 16 * wave < part.hi && static_cast<uint32_t>(part_entry) < pages;
+    const int64_t ph = int64_t(part_there ? part_entry : 0) * heads + head;
+    ksr = a.ks[ph];
+    vsr = a.vs[ph];
   };
-  auto stage = [&](int buf, int index) {
-    uint8_t* kb = sh + buf * kBuf;
+  // Before its codes are widened into LDS, a tile may need repairs: codes of 0 for
+  // what is not there, a look at the values that are hidden from some row, its scales.
+  auto repair = [&](int buf, int index) {
     const int32_t k0 = part.lo + kBK * index;
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       const int key = sk + (kBK / NP) * i;
-      if (__any(!there[i])) {  // what is not there has codes of 0
+      if (__any(!there[i])) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           kr[i][e] = there[i] ? kr[i][e] : 0u;
           vr[i][e] = there[i] ? vr[i][e] : 0u;
         }
       }
-      if (k0 < all_lo || k0 + kBK > all_hi) {  // hidden from some row: not finite counts
+      if (k0 < all_lo || k0 + kBK > all_hi) {
         uint32_t odd = 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -619,27 +633,34 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs a, Cut cut, i
         }
         if (odd) sh_odd[buf] = index;
       }
-      *reinterpret_cast<u32x4*>(kb + key_at<D>(key, 2 * sp)) = bf16_of<F>(kr[i][0], kr[i][1]);
-      *reinterpret_cast<u32x4*>(kb + key_at<D>(key, 2 * sp + 1)) = bf16_of<F>(kr[i][2], kr[i][3]);
-      u32x4* v = reinterpret_cast<u32x4*>(kb + 2 * kBuf + val_at<D>(key, 32 * sp));
-      v[0] = f16_of<F>(vr[i][0], vr[i][1]);
-      v[1] = f16_of<F>(vr[i][2], vr[i][3]);
-      if (scaler) {
-        const PartScale ps = part_scale(there[i], ksr[i], vsr[i], sm);
-        sh_p[buf][key / 16] = make_float4(ps.c, ps.lv, ps.inv, 0.0f);
-        if (there[i] && !finite_scales(ksr[i], vsr[i])) sh_bad[buf] = index;
-      }
+    }
+    const PartScale ps = part_scale(part_there, ksr, vsr, sm);
+    const float bad = part_there && !finite_scales(ksr, vsr) ? 1.0f : 0.0f;
+    if (lane == 0) sh_p[buf][wave] = make_float4(ps.c, ps.lv, ps.inv, bad);
+  };
+  const uint32_t kst0 = key_at<D>(sk, 2 * sp), kst1 = key_at<D>(sk, 2 * sp + 1), vst = 2 * kBuf + val_at<D>(sk, 32 * sp);
+  auto stage = [&](int buf, int share, int shares) {  // one of `shares` equal shares of the widening
+    const uint32_t at = buf * kBuf;
+#pragma unroll
+    for (int u = 4 * NP * share / shares; u < 4 * NP * (share + 1) / shares; ++u) {
+      const int i = u / 4, x = u % 2 * 2;
+      uint8_t* row = sh + (kBK / NP) * i * (2 * D);
+      if (u % 4 < 2)
+        *reinterpret_cast<u32x4*>(row + ((x ? kst1 : kst0) + at)) = bf16_of<F>(kr[i][x], kr[i][x + 1]);
+      else
+        *reinterpret_cast<u32x4*>(row + (vst + at) + 8 * x) = f16_of<F>(vr[i][x], vr[i][x + 1]);
     }
   };
   const int32_t steps = (part.hi - part.lo + kBK - 1) / kBK;
-  if (threadIdx.x < 2) sh_odd[threadIdx.x] = sh_bad[threadIdx.x] = -1;
+  if (threadIdx.x < 2) sh_odd[threadIdx.x] = -1;
   __syncthreads();
   bool redo = false;
   if (steps > 0) {
     look_up(part.lo);
     fetch(part.lo);
     look_up(part.lo + kBK);
-    stage(0, 0);
+    repair(0, 0);
+    stage(0, 0, 1);
   }
   __syncthreads();
   for (int32_t t = 0; t < steps; ++t) {
@@ -649,86 +670,135 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs a, Cut cut, i
       fetch(k0 + kBK);
       look_up(k0 + 2 * kBK);
     }
+    const bool more = t + 1 < steps;
     if (k0 < w_any.hi && k0 + kBK > w_any.lo) {
       const uint32_t at = buf * kBuf;
+      const bool edge = k0 < w_all.lo || k0 + kBK > w_all.hi || k0 + kBK > part.hi;
       auto key_of = [&](int kt, int i) {
         return *reinterpret_cast<const bf16x8*>(sh + (ka[i] + at) + 32 * kt * (2 * D));
       };
-      f32x16 z[2] = {};
-      bf16x8 kf[KS];
-#pragma unroll
-      for (int i = 0; i < KS; ++i) kf[i] = key_of(0, i);
-#pragma unroll
-      for (int i = 0; i < KS; ++i) {
-        z[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[i], __builtin_bit_cast(bf16x8, q[i]), z[0], 0, 0, 0);
-        kf[i] = key_of(1, i);
-      }
-#pragma unroll
-      for (int i = 0; i < KS; ++i)
-        z[1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[i], __builtin_bit_cast(bf16x8, q[i]), z[1], 0, 0, 0);
-      float4 ps[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) ps[i] = sh_p[buf][i];
-      // register 8 e + i of part 2 kt + e is key 32 kt + 16 e + 8 (i / 4) + 4 h + i % 4
-      const bool edge = k0 < w_all.lo || k0 + kBK > w_all.hi || k0 + kBK > part.hi;
-      redo = redo || sh_bad[buf] == t || (edge && sh_odd[buf] == t);
-      if (edge) {
-        const int32_t from = see.lo - k0 - 4 * h;
-        const uint32_t n = see.hi - see.lo;
-#pragma unroll
-        for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            z[kt][i] = static_cast<uint32_t>(32 * kt + 8 * (i / 4) + i % 4 - from) < n ? z[kt][i] : -INFINITY;
-      }
-      f16x8 pf[4];   // weights of the tile's 16-key parts
-      float sum[4];  // this lane's sums of them
-      auto weigh = [&] {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float lift = ps[e].y - m;
-          float w[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) w[i] = exp2_fast(fmaf(z[e / 2][8 * (e % 2) + i], ps[e].x, lift));
-          sum[e] = ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
-          pf[e] = __builtin_bit_cast(f16x8, (u32x4{pack_f16(w[0], w[1]), pack_f16(w[2], w[3]), pack_f16(w[4], w[5]),
-                                                   pack_f16(w[6], w[7])}));
-        }
-      };
-      weigh();
-      if (__any(!(fmaxf(fmaxf(sum[0], sum[1]), fmaxf(sum[2], sum[3])) < kFull))) {
-        float top = kNoKey;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x = fmaxf(x, z[e / 2][8 * (e % 2) + i]);
-          top = fmaxf(top, fmaf(x, ps[e].x, ps[e].y));
-        }
-        top = fmaxf(top, __shfl_xor(top, 32));
-        const float mn = fmaxf(m, top);
-        const float fade = exp2_fast(m - mn);
-        l *= fade;
-#pragma unroll
-        for (int d = 0; d < DT; ++d) o[d] *= fade;
-        m = mn;
-        weigh();
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) l = fmaf(sum[e], ps[e].z, l);
       // values of part e, output tile d: keys 16 e + {0..3, 8..11} + 4 h, dimension 32 d + c
       auto value_of = [&](int e, int d) {
         const uint8_t* v = sh + (va[d] + at);
         const u32x2 lo = read_tr(v + 16 * e * (2 * D)), hi = read_tr(v + (16 * e + 8) * (2 * D));
         return __builtin_bit_cast(f16x8, (u32x4{lo[0], lo[1], hi[0], hi[1]}));
       };
+      // register 8 e + i of part 2 kt + e is key 32 kt + 16 e + 8 (i / 4) + 4 h + i % 4
+      f32x16 z[2] = {};
+      auto hide = [&](int kt) {
+        const int32_t from = see.lo - k0 - 4 * h;
+        const uint32_t n = see.hi - see.lo;
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
+        for (int i = 0; i < 16; ++i)
+          z[kt][i] = static_cast<uint32_t>(32 * kt + 8 * (i / 4) + i % 4 - from) < n ? z[kt][i] : -INFINITY;
+      };
+      float pc[4], plv[4], pinv[4];  // the scales of the tile's 16-key parts, the same in every lane
+      u32x4 pw[4];   // weights of the parts
+      float sum[4];  // this lane's sums of them
+      auto weigh = [&](int kt, int i, int n) {  // scores i .. i + n of half kt
 #pragma unroll
-        for (int d = 0; d < DT; ++d)
-          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(value_of(e, d), pf[e], o[d], 0, 0, 0);
+        for (int k = i; k < i + n; k += 2) {
+          const int e = 2 * kt + k / 8;
+          const float w0 = exp2_fast(fmaf(z[kt][k], pc[e], plv[e] - m)), w1 = exp2_fast(fmaf(z[kt][k + 1], pc[e], plv[e] - m));
+          sum[e] = k % 8 == 0 ? w0 + w1 : sum[e] + (w0 + w1);
+          pw[e][k % 8 / 2] = pack_f16(w0, w1);
+        }
+      };
+      auto follow = [&](int kt) {  // too large for fp16: m follows the maximum
+        if (__any(!(fmaxf(sum[2 * kt], sum[2 * kt + 1]) < kFull))) {
+          float top = kNoKey;
+#pragma unroll
+          for (int e = 2 * kt; e < 2 * kt + 2; ++e) {
+            float x = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x = fmaxf(x, z[kt][8 * (e % 2) + i]);
+            top = fmaxf(top, fmaf(x, pc[e], plv[e]));
+          }
+          top = fmaxf(top, __shfl_xor(top, 32));
+          const float mn = fmaxf(m, top);
+          const float fade = exp2_fast(m - mn);
+          l *= fade;
+#pragma unroll
+          for (int d = 0; d < DT; ++d) o[d] *= fade;
+          m = mn;
+          weigh(kt, 0, 16);
+        }
+        l = fmaf(sum[2 * kt], pinv[2 * kt], l);
+        l = fmaf(sum[2 * kt + 1], pinv[2 * kt + 1], l);
+      };
+      // The matrix cores' work on one half of the tile runs under the exponentials of the
+      // other, and the last products under the widening of the next tile: a matrix
+      // instruction takes 8 passes of 4 cycles, in which this wave issues other work.
+      constexpr int kAhead = 3;  // operands read ahead of their use
+      bf16x8 kf[KS];
+      auto scores = [&](int kt, auto&& under) {
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+          if (i + kAhead < KS) kf[i + kAhead] = key_of(kt, i + kAhead);
+          z[kt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[i], __builtin_bit_cast(bf16x8, q[i]), z[kt], 0, 0, 0);
+          under(i);
+          pin();
+        }
+      };
+      f16x8 vf[2 * DT];
+      auto add = [&](int kt, auto&& under) {
+#pragma unroll
+        for (int i = 0; i < 2 * DT; ++i) {
+          if (i + kAhead < 2 * DT) vf[i + kAhead] = value_of(2 * kt + (i + kAhead) / DT, (i + kAhead) % DT);
+          o[i % DT] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[i], __builtin_bit_cast(f16x8, pw[2 * kt + i / DT]),
+                                                             o[i % DT], 0, 0, 0);
+          under(i);
+          pin();
+        }
+      };
+      auto ahead_k = [&](int kt) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) kf[i] = key_of(kt, i);
+      };
+      auto ahead_v = [&](int kt) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) vf[i] = value_of(2 * kt + i / DT, i % DT);
+      };
+      ahead_k(0);
+      float4 ps[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) ps[e] = sh_p[buf][e];
+      pin();
+      scores(0, [&](int i) {
+        if (i == KS - 1) ahead_k(1);
+      });
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        pc[e] = uniform(ps[e].x);
+        plv[e] = uniform(ps[e].y);
+        pinv[e] = uniform(ps[e].z);
+        redo = redo || uniform(ps[e].w) != 0.0f;
+      }
+      if (edge) {
+        redo = redo || sh_odd[buf] == t;
+        hide(0);
+      }
+      scores(1, [&](int i) {
+        weigh(0, 16 / KS * i, 16 / KS);
+        if (i == KS - 1) ahead_v(0);
+      });
+      follow(0);
+      if (edge) hide(1);
+      add(0, [&](int i) {
+        weigh(1, 16 / (2 * DT) * i, 16 / (2 * DT));
+        if (i == 2 * DT - 1) ahead_v(1);
+      });
+      follow(1);
+      if (more) {
+        repair(buf ^ 1, t + 1);
+        add(1, [&](int i) { stage(buf ^ 1, i, 2 * DT); });
+      } else {
+        add(1, [](int) {});
+      }
+    } else if (more) {
+      repair(buf ^ 1, t + 1);
+      stage(buf ^ 1, 0, 1);
     }
-    if (t + 1 < steps) stage(buf ^ 1, t + 1);
     __syncthreads();
   }
   if (redo) {
