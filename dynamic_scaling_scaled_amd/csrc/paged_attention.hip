@@ -98,6 +98,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 __device__ __forceinline__ float uniform(float x) {
   return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(x)));
 }
+// 0 in a vector register, of which the compiler knows only that it is an integer.
+__device__ __forceinline__ int hidden_zero() {
+  int z;
+  asm("v_mov_b32 %0, 0" : "=v"(z));
+  return z;
+}
 // Keeps the compiler from moving instructions across this point: the kernels' loops
 // say themselves which work runs under which matrix instruction.
 __device__ __forceinline__ void pin() { __builtin_amdgcn_sched_barrier(0); }
@@ -569,74 +575,70 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs a, Cut cut, i
   for (int d = 0; d < DT; ++d)  // keys 4 h + (lane & 15) / 4, dimensions 32 d + 16 (lane / 16 & 1) + 4 (lane & 3)
     va[d] = 2 * kBuf + val_at<D>(4 * h + (lane & 15) / 4, 64 * d + 32 * ((lane >> 4) & 1) + 8 * (lane & 3));
 
-  // staging: this thread's pieces are bytes [16 sp, 16 sp + 16) of keys sk + 64 / NP * i
-  constexpr int TK = D / 16;  // threads of a key
+  // staging: this thread's pieces are bytes [16 sp, 16 sp + 16) of keys sk + 64 / NP * i.  A wave's
+  // keys of one piece lie in one 16-key part, so its page is the same for all lanes.
+  constexpr int TK = D / 16;           // threads of a key
+  constexpr int PK = kBK / NP;         // keys between a thread's pieces
+  constexpr int WK = 64 / TK;          // keys of a wave's piece
   const int sk = threadIdx.x / TK, sp = threadIdx.x % TK;
-  const int32_t* table = a.p.table + b * a.p.ld_table;
-  const uint32_t page_bytes = static_cast<uint32_t>(page) * D, pitch = page_bytes * heads;
-  const uint32_t pages = static_cast<uint32_t>(a.p.pages);
-  uint64_t lane_at[NP];  // the piece's place in its page (a tile starts at a multiple of 64)
-#pragma unroll
-  for (int i = 0; i < NP; ++i)
-    lane_at[i] = uint64_t(head) * page_bytes + ((sk + (kBK / NP) * i) & (page - 1)) * D + 16 * sp;
+  const uint32_t lane_at = (lane / TK) * D + 16 * sp;
+  const int mine = NP == 2 ? wave & 1 : 0;                            // the piece whose part's scales this wave takes
+  const int mine_part = NP == 2 ? (wave >> 1) + 2 * (wave & 1) : wave;
+  // looked up by vector loads, which retire in order with the tiles' (a scalar load
+  // would make every wait for an LDS read wait for it too)
+  const int32_t* table = a.p.table + b * a.p.ld_table + hidden_zero();
+  const uint32_t page_bytes = static_cast<uint32_t>(page) * D, pages = static_cast<uint32_t>(a.p.pages);
   u32x4 kr[NP], vr[NP];
   int32_t entry[NP];   // table entries of the pieces fetched next
-  bool there[NP];      // the page of the piece fetched last is present, and the position exists
-  // This wave looks after the scales of the tile's 16-key part number `wave`, in scalars.
-  int32_t part_entry;
+  bool there[NP];      // the page of the piece fetched last is present
   float ksr, vsr;
-  bool part_there;
   // (positions past the end look up the last page: every load is of a page of the table)
   auto look_up = [&](int32_t k0) {
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      const int32_t j = k0 + sk + (kBK / NP) * i;
+      const int32_t j = k0 + WK * wave + PK * i;
       entry[i] = table[(j < part.hi ? j : part.hi - 1) >> shift];
     }
-    const int32_t j = k0 + 16 * wave;
-    part_entry = table[(j < part.hi ? j : part.hi - 1) >> shift];
   };
   auto fetch = [&](int32_t k0) {
-    const int32_t inside = (k0 & (page - 1) & kBK) * D;  // pages of 128: their second half
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      there[i] = k0 + sk + (kBK / NP) * i < part.hi && static_cast<uint32_t>(entry[i]) < pages;
-      const uint64_t at = uint64_t(there[i] ? static_cast<uint32_t>(entry[i]) : 0u) * pitch + lane_at[i];
-      kr[i] = *reinterpret_cast<const u32x4*>(a.kc + inside + at);
-      vr[i] = *reinterpret_cast<const u32x4*>(a.vc + inside + at);
+      const int32_t j = k0 + WK * wave + PK * i;
+      const uint32_t pg = __builtin_amdgcn_readfirstlane(entry[i]);
+      there[i] = pg < pages;
+      const uint64_t ph = uint64_t(there[i] ? pg : 0u) * static_cast<uint32_t>(heads) + static_cast<uint32_t>(head);
+      const uint64_t at = ph * page_bytes + static_cast<uint32_t>((j & (page - 1)) * D);
+      kr[i] = *reinterpret_cast<const u32x4*>(a.kc + at + lane_at);
+      vr[i] = *reinterpret_cast<const u32x4*>(a.vc + at + lane_at);
+      if (i == mine) {
+        ksr = (a.ks + ph)[hidden_zero()];
+        vsr = (a.vs + ph)[hidden_zero()];
+      }
     }
-    part_there = k0 + 16 * wave < part.hi && static_cast<uint32_t>(part_entry) < pages;
-    const int64_t ph = int64_t(part_there ? part_entry : 0) * heads + head;
-    ksr = a.ks[ph];
-    vsr = a.vs[ph];
   };
-  // Before its codes are widened into LDS, a tile may need repairs: codes of 0 for
-  // what is not there, a look at the values that are hidden from some row, its scales.
+  // Before its codes are widened into LDS, a tile may need repairs: codes of 0 for pages that
+  // are not there and for values that no row sees, a look at the values that some row does not
+  // see; and its scales.  (Keys past the end need none: their scores are hidden.)
   auto repair = [&](int buf, int index) {
     const int32_t k0 = part.lo + kBK * index;
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      const int key = sk + (kBK / NP) * i;
-      if (__any(!there[i])) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          kr[i][e] = there[i] ? kr[i][e] : 0u;
-          vr[i][e] = there[i] ? vr[i][e] : 0u;
-        }
-      }
-      if (k0 < all_lo || k0 + kBK > all_hi) {
+      if (!there[i]) kr[i] = vr[i] = u32x4{0u, 0u, 0u, 0u};
+      if (k0 < all_lo || k0 + kBK > all_hi || k0 + kBK > part.hi) {
+        const int32_t key = k0 + sk + PK * i;
         uint32_t odd = 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          vr[i][e] = k0 + key >= any_lo ? vr[i][e] : 0u;
+          vr[i][e] = key >= any_lo && key < part.hi ? vr[i][e] : 0u;
           odd |= non_finite<F>(vr[i][e]);
         }
         if (odd) sh_odd[buf] = index;
       }
     }
-    const PartScale ps = part_scale(part_there, ksr, vsr, sm);
-    const float bad = part_there && !finite_scales(ksr, vsr) ? 1.0f : 0.0f;
-    if (lane == 0) sh_p[buf][wave] = make_float4(ps.c, ps.lv, ps.inv, bad);
+    const bool here = there[mine];
+    const PartScale ps = part_scale(here, ksr, vsr, sm);
+    if (lane == 0)
+      sh_p[buf][mine_part] = make_float4(ps.c, ps.lv, ps.inv, here && !finite_scales(ksr, vsr) ? 1.0f : 0.0f);
   };
   const uint32_t kst0 = key_at<D>(sk, 2 * sp), kst1 = key_at<D>(sk, 2 * sp + 1), vst = 2 * kBuf + val_at<D>(sk, 32 * sp);
   auto stage = [&](int buf, int share, int shares) {  // one of `shares` equal shares of the widening
@@ -644,17 +646,17 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs a, Cut cut, i
 #pragma unroll
     for (int u = 4 * NP * share / shares; u < 4 * NP * (share + 1) / shares; ++u) {
       const int i = u / 4, x = u % 2 * 2;
-      uint8_t* row = sh + (kBK / NP) * i * (2 * D);
+      const uint32_t row = at + PK * i * (2 * D);
       if (u % 4 < 2)
-        *reinterpret_cast<u32x4*>(row + ((x ? kst1 : kst0) + at)) = bf16_of<F>(kr[i][x], kr[i][x + 1]);
+        *reinterpret_cast<u32x4*>(sh + (x ? kst1 : kst0) + row) = bf16_of<F>(kr[i][x], kr[i][x + 1]);
       else
-        *reinterpret_cast<u32x4*>(row + (vst + at) + 8 * x) = f16_of<F>(vr[i][x], vr[i][x + 1]);
+        *reinterpret_cast<u32x4*>(sh + vst + (row + 8 * x)) = f16_of<F>(vr[i][x], vr[i][x + 1]);
     }
   };
   const int32_t steps = (part.hi - part.lo + kBK - 1) / kBK;
   if (threadIdx.x < 2) sh_odd[threadIdx.x] = -1;
   __syncthreads();
-  bool redo = false;
+  int redo = 0;
   if (steps > 0) {
     look_up(part.lo);
     fetch(part.lo);
@@ -663,8 +665,8 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs a, Cut cut, i
     stage(0, 0, 1);
   }
   __syncthreads();
-  for (int32_t t = 0; t < steps; ++t) {
-    const int buf = t & 1;
+  auto step = [&](int32_t t, auto which) {
+    constexpr int buf = decltype(which)::value;
     const int32_t k0 = part.lo + kBK * t;
     if (t + 1 < steps) {
       fetch(k0 + kBK);
@@ -672,15 +674,15 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs a, Cut cut, i
     }
     const bool more = t + 1 < steps;
     if (k0 < w_any.hi && k0 + kBK > w_any.lo) {
-      const uint32_t at = buf * kBuf;
+      constexpr uint32_t at = buf * kBuf;
       const bool edge = k0 < w_all.lo || k0 + kBK > w_all.hi || k0 + kBK > part.hi;
       auto key_of = [&](int kt, int i) {
-        return *reinterpret_cast<const bf16x8*>(sh + (ka[i] + at) + 32 * kt * (2 * D));
+        return *reinterpret_cast<const bf16x8*>(sh + ka[i] + (at + 32 * kt * (2 * D)));
       };
       // values of part e, output tile d: keys 16 e + {0..3, 8..11} + 4 h, dimension 32 d + c
       auto value_of = [&](int e, int d) {
-        const uint8_t* v = sh + (va[d] + at);
-        const u32x2 lo = read_tr(v + 16 * e * (2 * D)), hi = read_tr(v + (16 * e + 8) * (2 * D));
+        const uint8_t* v = sh + va[d];
+        const u32x2 lo = read_tr(v + (at + 16 * e * (2 * D))), hi = read_tr(v + (at + (16 * e + 8) * (2 * D)));
         return __builtin_bit_cast(f16x8, (u32x4{lo[0], lo[1], hi[0], hi[1]}));
       };
       // register 8 e + i of part 2 kt + e is key 32 kt + 16 e + 8 (i / 4) + 4 h + i % 4
@@ -772,10 +774,10 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs a, Cut cut, i
         pc[e] = uniform(ps[e].x);
         plv[e] = uniform(ps[e].y);
         pinv[e] = uniform(ps[e].z);
-        redo = redo || uniform(ps[e].w) != 0.0f;
+        redo |= __builtin_amdgcn_readfirstlane(__float_as_int(ps[e].w));
       }
       if (edge) {
-        redo = redo || sh_odd[buf] == t;
+        redo |= sh_odd[buf] == t;
         hide(0);
       }
       scores(1, [&](int i) {
@@ -800,6 +802,10 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs a, Cut cut, i
       stage(buf ^ 1, 0, 1);
     }
     __syncthreads();
+  };
+  for (int32_t t = 0; t < steps; t += 2) {
+    step(t, std::integral_constant<int, 0>{});
+    if (t + 1 < steps) step(t + 1, std::integral_constant<int, 1>{});
   }
   if (redo) {
     for (int row = 0; row < wr; ++row) {
