@@ -894,12 +894,16 @@ hipError_t launch_paged_attention(const AttendArgs& a, hipStream_t st) {
   const int64_t tile_rows = few ? 16 : 128;
   const int64_t tiles = ceil_div(rows, tile_rows);
   const int64_t jobs = a.p.seqs * tiles * a.p.heads;  // workgroups without a cut
-  // Cut the keys when the jobs alone do not fill the card: chunks of at least 512 keys, about 8 workgroups per CU.
+  // Cut the keys when the jobs alone do not fill the card: decode to about 8
+  // workgroups per CU (ragged lengths even out), prompts to the 2 that a CU
+  // holds at once; chunks of at least 512 keys.  A window bounds what a causal tile can see.
   Cut cut{1, 64};
-  const int64_t want = ceil_div(int64_t(8) * device_cus(), jobs);
+  int64_t span = a.max_kv;
+  if (a.causal && a.window > 0) span = std::min(span, a.window + tile_rows / group + 64);
+  const int64_t want = ceil_div(int64_t(few ? 8 : 2) * device_cus(), jobs);
   if (want > 1) {
-    const int64_t len = std::max<int64_t>(512, ceil_div(ceil_div(a.max_kv, want), 64) * 64);
-    cut.chunks = static_cast<int32_t>(ceil_div(a.max_kv, len));
+    const int64_t len = std::max<int64_t>(512, ceil_div(ceil_div(span, want), 64) * 64);
+    cut.chunks = static_cast<int32_t>(ceil_div(span, len));
     cut.len = static_cast<int32_t>(len);
   }
   Parts parts{nullptr, nullptr};
