@@ -128,17 +128,34 @@ __device__ __forceinline__ Range visible(const AttendArgs& a, const SeqSpan& s, 
 // What a tile of `rows` query rows from row r0 sees together (its first row
 // starts first, its last row ends last), from a multiple of 64 on.
 __device__ __forceinline__ Range tile_range(const AttendArgs& a, const SeqSpan& s, int32_t r0, int32_t rows,
-                                            int32_t group) {
-  const int64_t last = (int64_t(r0) + rows - 1) / group;
-  const Range x = visible(a, s, r0 / group), y = visible(a, s, last < s.n ? last : s.n - 1);
-  return Range{x.lo / 64 * 64, y.hi};
+                                            const FastDiv& group) {
+  const Range x = visible(a, s, group.div(r0)), y = visible(a, s, group.div(r0 + rows - 1));
+  return Range{x.lo & ~63, y.hi};
 }
 
 // How the keys of a tile are cut: `chunks` pieces of `len` keys (a multiple
-// of 64), the last one open-ended.
+// of 64), the last one open-ended.  And the divisors of the grid: a workgroup's
+// start is dependent loads and index arithmetic, which the 64-bit quotients dominated.
 struct Cut {
   int32_t chunks, len;
+  FastDiv by_heads, by_tiles, by_chunks, by_group;
 };
+
+// Workgroup -> (sequence, chunk, tile, head), head fastest: neighbours read
+// neighbouring parts of the same pages, and with 8 heads each XCD's L2 keeps one of them.
+struct Place {
+  uint32_t head, tile, chunk, b;
+};
+__device__ __forceinline__ Place place_of(uint32_t blk, const Cut& c) {
+  Place p;
+  uint32_t x = c.by_heads.div(blk);
+  p.head = blk - x * c.by_heads.d;
+  uint32_t y = c.by_tiles.div(x);
+  p.tile = x - y * c.by_tiles.d;
+  p.b = c.by_chunks.div(y);
+  p.chunk = y - p.b * c.by_chunks.d;
+  return p;
+}
 
 __device__ __forceinline__ Range chunk_of(const Range& t, const Cut& c, int32_t i) {
   const int64_t lo = int64_t(t.lo) + int64_t(i) * c.len, hi = lo + c.len;
@@ -250,9 +267,13 @@ __device__ void careful_store(const AttendArgs& a, const Parts& parts, int32_t c
 // step go from HBM to registers in operand order: lane l (c = l % 16, g = l / 16)
 // loads 16-byte pieces of key c of each 16-key part, and for the keys
 // {4g..4g+3, 16+4g..16+4g+3}, whose scores it will hold, D/16 bytes of the values.
-template <int F, int D, int W>
-__global__ void __launch_bounds__(64 * W, W == 4 ? 3 : 1)
-    k_attend_few(AttendArgs a, Cut cut, int32_t tiles, Parts parts) {
+// 8 waves a workgroup: 64 ragged sequences of up to 8192 tokens, 8 heads, in one piece each,
+// 114 us; 4 waves 124; 16 (which no longer fit the registers) 166.
+constexpr int kFewWaves = 8;
+
+template <int F, int D>
+__global__ void __launch_bounds__(64 * kFewWaves) k_attend_few(AttendArgs a, Cut cut, Parts parts) {
+  constexpr int W = kFewWaves;
   constexpr int KD = D / 64;      // 16-byte key pieces of a lane and part
   constexpr int VW = D / 64;      // dwords of a lane and key
   constexpr int DT = D / 16;      // 16-wide output tiles: tile 4w + b is byte b of dword w
@@ -262,31 +283,28 @@ __global__ void __launch_bounds__(64 * W, W == 4 ? 3 : 1)
   __shared__ int sh_redo[W];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
-  const int32_t heads = a.p.heads, group = static_cast<int32_t>(a.q_heads / heads);
-  int64_t blk = blockIdx.x;
-  const int32_t head = static_cast<int32_t>(blk % heads);
-  blk /= heads;
-  const int32_t chunk = static_cast<int32_t>(blk % cut.chunks);
-  blk /= cut.chunks;
-  const int32_t r0 = static_cast<int32_t>(blk % tiles) * 16;
-  const int64_t b = blk / tiles;
+  const int32_t heads = a.p.heads, group = static_cast<int32_t>(cut.by_group.d);
+  const Place place = place_of(blockIdx.x, cut);
+  const int32_t head = place.head, chunk = place.chunk, r0 = place.tile * 16;
+  const int64_t b = place.b;
   const SeqSpan s = seq_span(a.p, b);
   const int64_t all = int64_t(s.n) * group;
   if (r0 >= all) return;
   const int32_t rows = all - r0 < 16 ? static_cast<int32_t>(all - r0) : 16;
-  const Range tile = tile_range(a, s, r0, rows, group);
+  const Range tile = tile_range(a, s, r0, rows, cut.by_group);
   const Range part = chunk_of(tile, cut, chunk);
   if (chunk > 0 && part.lo >= part.hi) return;  // (chunk 0 also writes the rows that see nothing)
   const int32_t page = a.p.page, shift = 31 - __builtin_clz(page);
   // this lane's query row
   const int32_t r = r0 + (c < rows ? c : 0);
-  const int64_t tok = s.tok0 + r / group;
-  const int64_t qh = int64_t(head) * group + r % group;
-  Range see = visible(a, s, r / group);
+  const int32_t ti = cut.by_group.div(r);
+  const int64_t tok = s.tok0 + ti;
+  const int64_t qh = int64_t(head) * group + (r - ti * group);
+  Range see = visible(a, s, ti);
   see.hi = see.hi < part.hi ? see.hi : part.hi;
   if (c >= rows || see.hi < see.lo) see.hi = see.lo;
   // positions that every row sees, and that any row sees
-  const Range first = visible(a, s, r0 / group), last = visible(a, s, (r0 + rows - 1) / group);
+  const Range first = visible(a, s, cut.by_group.div(r0)), last = visible(a, s, cut.by_group.div(r0 + rows - 1));
   const int32_t all_lo = last.lo, all_hi = first.hi, any_lo = first.lo;
   const float sm = fabsf(a.sm_scale) * kLog2e;
   const uint32_t flip = a.sm_scale < 0.0f ? 0x80008000u : 0u;  // a negative scale negates the query
@@ -309,21 +327,35 @@ __global__ void __launch_bounds__(64 * W, W == 4 ? 3 : 1)
     int32_t pg[2];
     float ks[2], vs[2];
   };
+  // Table entries are looked up a step before their keys are loaded, the keys a step
+  // before they are used.  (Past the end the last page is looked up, and counts as absent.)
+  const int32_t* table = a.p.table + b * a.p.ld_table;
+  const uint32_t page_bytes = static_cast<uint32_t>(page) * D, pages = static_cast<uint32_t>(a.p.pages);
+  const uint32_t k_at = c * D + 16 * g, v_at = 4 * g * D + c * (D / 16);
+  int32_t entry[2];
+  auto look_up = [&](int32_t k0) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int32_t j = k0 + 16 * t;
+      entry[t] = table[(j < part.hi ? j : part.hi - 1) >> shift];
+    }
+  };
   auto load = [&](Step& st, int32_t k0) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const int32_t p0 = k0 + 16 * t, lp = p0 >> shift;
-      st.pg[t] = p0 < part.hi ? page_of(a.p, b, lp) : -1;
-      const int64_t at = int64_t(st.pg[t] < 0 ? 0 : st.pg[t]) * heads + head;
-      st.ks[t] = a.ks[at];
-      st.vs[t] = a.vs[at];
-      const int64_t base = (at * page + (p0 - lp * page)) * D;
+      const int32_t p0 = k0 + 16 * t;
+      const bool there = p0 < part.hi && static_cast<uint32_t>(entry[t]) < pages;
+      st.pg[t] = there ? entry[t] : -1;
+      const uint64_t ph = uint64_t(there ? static_cast<uint32_t>(entry[t]) : 0u) * static_cast<uint32_t>(heads) +
+                          static_cast<uint32_t>(head);
+      st.ks[t] = a.ks[ph];
+      st.vs[t] = a.vs[ph];
+      const uint64_t base = ph * page_bytes + static_cast<uint32_t>((p0 & (page - 1)) * D);
 #pragma unroll
-      for (int h = 0; h < KD; ++h)
-        st.k[t][h] = *reinterpret_cast<const u32x4*>(a.kc + base + c * D + 64 * h + 16 * g);
+      for (int h = 0; h < KD; ++h) st.k[t][h] = *reinterpret_cast<const u32x4*>(a.kc + base + k_at + 64 * h);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint8_t* p = a.vc + base + (4 * g + j) * D + c * (D / 16);
+        const uint8_t* p = a.vc + base + v_at + j * D;
         if constexpr (VW == 2) {
           const u32x2 x = *reinterpret_cast<const u32x2*>(p);
           st.v[4 * t + j][0] = x[0];
@@ -338,10 +370,15 @@ __global__ void __launch_bounds__(64 * W, W == 4 ? 3 : 1)
   uint32_t redo = 0;  // a hidden value, or one under such a scale, may be no finite number
   const int32_t begin = part.lo + 32 * wave;
   Step cur;
-  if (begin < part.hi) load(cur, begin);
+  if (begin < part.hi) {
+    look_up(begin);
+    load(cur, begin);
+    look_up(begin + 32 * W);
+  }
   for (int32_t k0 = begin; k0 < part.hi; k0 += 32 * W) {
     Step next;
-    load(next, k0 + 32 * W < part.hi ? k0 + 32 * W : k0);
+    load(next, k0 + 32 * W);
+    look_up(k0 + 64 * W);
     f32x4 z[2];
     PartScale ps[2];
 #pragma unroll
@@ -469,8 +506,8 @@ __global__ void __launch_bounds__(64 * W, W == 4 ? 3 : 1)
       lt += ml.y * f;
       y += *reinterpret_cast<const f32x4*>(&sh_o[w][row][d]) * f;
     }
-    const int32_t rr = r0 + row;
-    const int64_t t = s.tok0 + rr / group, h = int64_t(head) * group + rr % group;
+    const int32_t rr = r0 + row, ri = cut.by_group.div(rr);
+    const int64_t t = s.tok0 + ri, h = int64_t(head) * group + (rr - ri * group);
     if (cut.chunks == 1) {
       const float inv = lt != 0.0f ? 1.0f / lt : 0.0f;
       *reinterpret_cast<u32x2*>(a.y + t * a.ldy + h * a.hdy + d) =
@@ -511,7 +548,7 @@ __device__ __forceinline__ u32x2 read_tr(const uint8_t* p) {
 }
 
 template <int F, int D>
-__global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs a, Cut cut, int32_t tiles, Parts parts) {
+__global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs a, Cut cut, Parts parts) {
   constexpr int NP = D / 64;   // 16-byte pieces of keys, and of values, that a thread stages
   constexpr int KS = D / 16;   // matrix steps along the dimensions
   constexpr int DT = D / 32;   // 32-wide output tiles
@@ -521,35 +558,33 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs a, Cut cut, i
   __shared__ int sh_odd[2];                       // the last tile of this buffer with a value code that is not finite
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 31, h = lane >> 5;
-  const int32_t heads = a.p.heads, group = static_cast<int32_t>(a.q_heads / heads);
-  int64_t blk = blockIdx.x;
-  const int32_t head = static_cast<int32_t>(blk % heads);
-  blk /= heads;
-  const int32_t r0 = (tiles - 1 - static_cast<int32_t>(blk % tiles)) * 128;  // causal: the longest first
-  blk /= tiles;
-  const int32_t chunk = static_cast<int32_t>(blk % cut.chunks);
-  const int64_t b = blk / cut.chunks;
+  const int32_t heads = a.p.heads, group = static_cast<int32_t>(cut.by_group.d);
+  const Place place = place_of(blockIdx.x, cut);
+  const int32_t head = place.head, chunk = place.chunk;
+  const int32_t r0 = (cut.by_tiles.d - 1 - place.tile) * 128;  // causal: the longest first
+  const int64_t b = place.b;
   const SeqSpan s = seq_span(a.p, b);
   const int64_t all = int64_t(s.n) * group;
   if (r0 >= all) return;
   const int32_t rows = all - r0 < 128 ? static_cast<int32_t>(all - r0) : 128;
-  const Range tile = tile_range(a, s, r0, rows, group);
+  const Range tile = tile_range(a, s, r0, rows, cut.by_group);
   const Range part = chunk_of(tile, cut, chunk);
   if (chunk > 0 && part.lo >= part.hi) return;
   const int32_t page = a.p.page, shift = 31 - __builtin_clz(page);
   // positions that some row of the workgroup sees, that all of them see; the same for this wave
   const int32_t wr = rows - 32 * wave < 32 ? rows - 32 * wave : 32;  // rows of this wave (may be <= 0)
-  const Range wg_first = visible(a, s, r0 / group), wg_last = visible(a, s, (r0 + rows - 1) / group);
+  const Range wg_first = visible(a, s, cut.by_group.div(r0)), wg_last = visible(a, s, cut.by_group.div(r0 + rows - 1));
   const int32_t any_lo = wg_first.lo, all_lo = wg_last.lo, all_hi = wg_first.hi;
   const int32_t r = r0 + 32 * wave + (c < wr ? c : 0);  // this lane's query row
-  const int64_t tok = s.tok0 + (wr > 0 ? r / group : 0);
-  const int64_t qh = int64_t(head) * group + r % group;
+  const int32_t ti = wr > 0 ? cut.by_group.div(r) : 0;
+  const int64_t tok = s.tok0 + ti;
+  const int64_t qh = int64_t(head) * group + (wr > 0 ? r - ti * group : 0);
   Range see = {0, 0}, w_all = {0, 0}, w_any = {0, 0};
   if (wr > 0) {
-    const Range f = visible(a, s, (r0 + 32 * wave) / group), e = visible(a, s, (r0 + 32 * wave + wr - 1) / group);
+    const Range f = visible(a, s, cut.by_group.div(r0 + 32 * wave)), e = visible(a, s, cut.by_group.div(r0 + 32 * wave + wr - 1));
     w_all = Range{e.lo, f.hi};
     w_any = Range{f.lo, e.hi};
-    if (c < wr) see = visible(a, s, r / group);
+    if (c < wr) see = visible(a, s, ti);
     if (wr < 32) w_all.hi = w_all.lo;  // idle rows see nothing: every tile is an edge
     see.hi = see.hi < part.hi ? see.hi : part.hi;
     see.hi = see.hi > see.lo ? see.hi : see.lo;
@@ -844,45 +879,60 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs a, Cut cut, i
 }
 
 // ---------------------------------------------------------------------------
-// Adds the chunks of each query row (one wave a row): with M = max m_i,
-// y = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.
+// Adds the chunks of one query row: with M = max m_i,
+// y = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.  A workgroup takes one row,
+// D / 4 threads a chunk, so that 8 (D = 128) or 16 chunks are read at once: the kernel is a chain of
+// loads, and its length is what it costs.
 template <int D>
 __global__ void __launch_bounds__(256) k_attend_join(AttendArgs a, Cut cut, int32_t tile_rows, Parts parts) {
-  constexpr int E = D / 64;
-  const int lane = threadIdx.x & 63;
-  const int64_t b = blockIdx.y;
-  const int32_t group = static_cast<int32_t>(a.q_heads / a.p.heads);
+  constexpr int T = D / 4, G = 256 / T;  // threads of a chunk, chunks at once
+  __shared__ __align__(16) f32x4 sh_y[G][T];
+  __shared__ float2 sh_ml[G];
+  const int x = threadIdx.x % T, y = threadIdx.x / T;
+  const int32_t group = static_cast<int32_t>(cut.by_group.d);
+  const uint32_t per = static_cast<uint32_t>(a.p.max_new) * cut.by_heads.d;  // by_heads: of the queries here
+  const int64_t b = blockIdx.x / per;
+  const uint32_t rest = blockIdx.x - static_cast<uint32_t>(b) * per;
+  const int32_t i = cut.by_heads.div(rest), h = rest - i * cut.by_heads.d;
   const SeqSpan s = seq_span(a.p, b);
-  const int64_t x = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);  // (token, q head) of the sequence
-  const int64_t i = x / a.q_heads, h = x % a.q_heads;
   if (i >= s.n) return;
-  const int32_t r0 = static_cast<int32_t>((i * group + h % group) / tile_rows * tile_rows);
+  const int32_t hg = h - static_cast<int32_t>(cut.by_group.div(h)) * group;
+  const int32_t r0 = (i * group + hg) & ~(tile_rows - 1);
   const int64_t left = int64_t(s.n) * group - r0;
-  const Range tile = tile_range(a, s, r0, left < tile_rows ? static_cast<int32_t>(left) : tile_rows, group);
-  int64_t n = (int64_t(tile.hi) - tile.lo + cut.len - 1) / cut.len;
+  const Range tile = tile_range(a, s, r0, left < tile_rows ? static_cast<int32_t>(left) : tile_rows, cut.by_group);
+  int32_t n = (int64_t(tile.hi) - tile.lo + cut.len - 1) / cut.len;
   n = n < 1 ? 1 : n > cut.chunks ? cut.chunks : n;
-  const int64_t tok = s.tok0 + i, row = tok * a.q_heads + h, step = a.p.tokens * a.q_heads;
-  float base = kNoKey;
-  for (int64_t k = lane; k < n; k += 64) base = fmaxf(base, parts.ml[k * step + row].x);
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) base = fmaxf(base, __shfl_xor(base, d));
-  float l = 0.0f, y[E] = {};
+  const int64_t row = (s.tok0 + i) * a.q_heads + h, step = a.p.tokens * a.q_heads;
+  float m = kNoKey, l = 0.0f;
+  f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
-  for (int64_t k = 0; k < n; ++k) {
+  for (int32_t k = y; k < n; k += G) {
     const float2 ml = parts.ml[k * step + row];
-    const float f = exp2_fast(ml.x - base);
-    l += ml.y * f;
-    const float* o = parts.o + (k * step + row) * D + lane * E;
+    const f32x4 v = *reinterpret_cast<const f32x4*>(parts.o + (k * step + row) * D + 4 * x);
+    const float mn = fmaxf(m, ml.x), fa = exp2_fast(m - mn), fb = exp2_fast(ml.x - mn);
+    l = l * fa + ml.y * fb;
+    o = o * fa + v * fb;
+    m = mn;
+  }
+  sh_y[y][x] = o;
+  if (x == 0) sh_ml[y] = make_float2(m, l);
+  __syncthreads();
+  if (y != 0) return;
+  float base = kNoKey;
 #pragma unroll
-    for (int e = 0; e < E; ++e) y[e] += o[e] * f;
+  for (int k = 0; k < G; ++k) base = fmaxf(base, sh_ml[k].x);
+  l = 0.0f;
+  o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int k = 0; k < G; ++k) {
+    const float f = exp2_fast(sh_ml[k].x - base);
+    l += sh_ml[k].y * f;
+    o += sh_y[k][x] * f;
   }
   const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-  uint16_t* out = a.y + tok * a.ldy + h * a.hdy + lane * E;
-  if constexpr (E == 2)
-    *reinterpret_cast<uint32_t*>(out) = pack_bf16(y[0] * inv, y[1] * inv);
-  else
-    *out = static_cast<uint16_t>(pack_bf16(y[0] * inv, 0.0f));
-  if (a.lse && lane == 0) a.lse[row] = l != 0.0f ? (base + log2_fast(l)) * kLn2 : -INFINITY;
+  *reinterpret_cast<u32x2*>(a.y + (s.tok0 + i) * a.ldy + h * a.hdy + 4 * x) =
+      u32x2{pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
+  if (a.lse && x == 0) a.lse[row] = l != 0.0f ? (base + log2_fast(l)) * kLn2 : -INFINITY;
 }
 
 }  // namespace
@@ -894,15 +944,20 @@ hipError_t launch_paged_attention(const AttendArgs& a, hipStream_t st) {
   const int64_t tile_rows = few ? 16 : 128;
   const int64_t tiles = ceil_div(rows, tile_rows);
   const int64_t jobs = a.p.seqs * tiles * a.p.heads;  // workgroups without a cut
-  // Cut the keys when the jobs alone do not fill the card: decode to about 8
-  // workgroups per CU (ragged lengths even out), prompts to the 2 that a CU
-  // holds at once; chunks of at least 512 keys.  A window bounds what a causal tile can see.
-  Cut cut{1, 64};
+  // Cut the keys when the jobs alone do not fill the card.  Prompts: to the 2
+  // workgroups that a CU holds.  Decode (1 a CU): a long stream per workgroup costs least (two
+  // sequences of 131072 tokens, 8 heads: 92 us in 256 chunks, 101 in 2048, and the parts' addition
+  // 5 and 7 us), so 1 a CU, and 2 from 8 sequences on, whose ragged lengths then even out; chunks of at least
+  // 1024 keys, below which a second launch costs more than the first saves (1001 keys: 10.6 us uncut,
+  // 8.6 + 3.9 in halves).  A window bounds what a causal tile can see.
+  Cut cut;
+  cut.chunks = 1;
+  cut.len = 64;
   int64_t span = a.max_kv;
   if (a.causal && a.window > 0) span = std::min(span, a.window + tile_rows / group + 64);
-  const int64_t want = ceil_div(int64_t(few ? 8 : 2) * device_cus(), jobs);
+  const int64_t want = ceil_div(int64_t(few && a.p.seqs < 8 ? 1 : 2) * device_cus(), jobs);
   if (want > 1) {
-    const int64_t len = std::max<int64_t>(512, ceil_div(ceil_div(span, want), 64) * 64);
+    const int64_t len = std::max<int64_t>(few ? 1024 : 512, ceil_div(ceil_div(span, want), 64) * 64);
     cut.chunks = static_cast<int32_t>(ceil_div(span, len));
     cut.len = static_cast<int32_t>(len);
   }
@@ -916,12 +971,16 @@ hipError_t launch_paged_attention(const AttendArgs& a, hipStream_t st) {
     parts.ml = reinterpret_cast<float2*>(parts.o + n * a.p.dim);
   }
   const int64_t grid = jobs * cut.chunks;
-  const int32_t nt = static_cast<int32_t>(tiles);
-  auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(grid), dim3(256), 0, st, a, cut, nt, parts); };
+  cut.by_heads = FastDiv(a.p.heads);
+  cut.by_tiles = FastDiv(static_cast<uint32_t>(tiles));
+  cut.by_chunks = FastDiv(cut.chunks);
+  cut.by_group = FastDiv(static_cast<uint32_t>(group));
+  const int waves = few ? kFewWaves : 4;
+  auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(grid), dim3(64 * waves), 0, st, a, cut, parts); };
   auto by_dim = [&](auto f) {
     constexpr int F = decltype(f)::value;
     if (few)
-      a.p.dim == 128 ? go(k_attend_few<F, 128, 4>) : go(k_attend_few<F, 64, 4>);
+      a.p.dim == 128 ? go(k_attend_few<F, 128>) : go(k_attend_few<F, 64>);
     else
       a.p.dim == 128 ? go(k_attend_many<F, 128>) : go(k_attend_many<F, 64>);
   };
@@ -931,7 +990,8 @@ hipError_t launch_paged_attention(const AttendArgs& a, hipStream_t st) {
     by_dim(std::integral_constant<int, kE5M2>{});
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && cut.chunks > 1) {
-    const dim3 jg(static_cast<uint32_t>(ceil_div(a.p.max_new * a.q_heads, 4)), static_cast<uint32_t>(a.p.seqs));
+    cut.by_heads = FastDiv(static_cast<uint32_t>(a.q_heads));
+    const dim3 jg(static_cast<uint32_t>(a.p.seqs * a.p.max_new * a.q_heads));
     auto join = [&](auto kern) {
       hipLaunchKernelGGL(kern, jg, dim3(256), 0, st, a, cut, static_cast<int32_t>(tile_rows), parts);
     };
