@@ -15,23 +15,23 @@ namespace {
 constexpr int kWaves = 4;
 
 template <typename T, int F, int D>
-__global__ void __launch_bounds__(64 * kWaves) k_kv_append(AppendArgs a, int pages_per_seq) {
+__global__ void __launch_bounds__(64 * kWaves) k_kv_append(AppendArgs a, FastDiv pages_per_seq) {
   constexpr int L = D / 8;         // lanes of one token (an octet each)
   constexpr int kTok = 64 / L;     // tokens of one wave instruction
   const int lane = threadIdx.x & 63;
-  const int64_t b = blockIdx.x / pages_per_seq;
-  const int pi = blockIdx.x % pages_per_seq;
+  const uint32_t b = pages_per_seq.div(blockIdx.x);
+  const int pi = blockIdx.x - b * pages_per_seq.d;
   const int item = blockIdx.y * kWaves + (threadIdx.x >> 6);  // head, then keys / values
   if (item >= 2 * a.p.heads) return;
   const bool val = item >= a.p.heads;
   const int head = val ? item - a.p.heads : item;
   const SeqSpan s = seq_span(a.p, b);
-  const int page = a.p.page;
+  const int page = a.p.page, shift = 31 - __builtin_clz(page);
   // positions [lo, hi) of the new tokens that exist, then of those in this page
   int64_t lo = s.first > 0 ? s.first : 0, hi = s.first + s.n < s.len ? s.first + s.n : s.len;
   if (lo >= hi) return;
-  const int64_t lp = lo / page + pi;
-  const int64_t p0 = lp * page;
+  const int64_t lp = (lo >> shift) + pi;
+  const int64_t p0 = lp << shift;
   const int64_t before = lo;  // positions below it were there before this call
   lo = lo > p0 ? lo : p0;
   hi = hi < p0 + page ? hi : p0 + page;
@@ -47,8 +47,19 @@ __global__ void __launch_bounds__(64 * kWaves) k_kv_append(AppendArgs a, int pag
   float* scp = (val ? a.vs : a.ks) + int64_t(pg) * a.p.heads + head;
   const int t0 = lane / L;
 
+  // the first kHeld octets of a lane (32 tokens at D = 128, 64 at D = 64) stay in registers,
+  // what a larger page brings beyond them is read again, from the cache
+  constexpr int kHeld = 8;
+  Octet<T> held[kHeld];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int t = t0 + i * kTok;
+    held[i].load(src + (t < n ? t : 0) * ld);  // (the maximum does not mind the first token again)
+  }
   uint32_t m = 0;
-  for (int t = t0; t < n; t += kTok) {
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) m = max(m, held[i].absmax_bits());
+  for (int t = t0 + kHeld * kTok; t < n; t += kTok) {
     Octet<T> o;
     o.load(src + t * ld);
     m = max(m, o.absmax_bits());
@@ -78,12 +89,18 @@ __global__ void __launch_bounds__(64 * kWaves) k_kv_append(AppendArgs a, int pag
   }
   if (lane == 0) *scp = sc;
   const int slot = static_cast<int>(lo - p0);
-  for (int t = t0; t < n; t += kTok) {
-    Octet<T> o;
-    o.load(src + t * ld);
+  auto put = [&](const Octet<T>& o, int t) {
     const u32x2 c = u32x2{cvt4_nan<F>(o.get(0) * r, o.get(1) * r, o.get(2) * r, o.get(3) * r),
                           cvt4_nan<F>(o.get(4) * r, o.get(5) * r, o.get(6) * r, o.get(7) * r)};
     *reinterpret_cast<u32x2*>(dst + (slot + t) * D + (lane % L) * 8) = c;
+  };
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if (t0 + i * kTok < n) put(held[i], t0 + i * kTok);
+  for (int t = t0 + kHeld * kTok; t < n; t += kTok) {
+    Octet<T> o;
+    o.load(src + t * ld);
+    put(o, t);
   }
 }
 
@@ -93,7 +110,7 @@ hipError_t launch_kv_append(const AppendArgs& a, hipStream_t st) {
   const int per = static_cast<int>((a.p.max_new + a.p.page - 2) / a.p.page + 1);  // pages that max_new tokens can touch
   const int64_t gx = a.p.seqs * per;
   const dim3 grid(static_cast<uint32_t>(gx), static_cast<uint32_t>(ceil_div(2 * a.p.heads, kWaves)));
-  auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, dim3(64 * kWaves), 0, st, a, per); };
+  auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, dim3(64 * kWaves), 0, st, a, FastDiv(per)); };
   auto by_fmt = [&](auto tag) {
     using T = decltype(tag);
     if (a.p.fmt == FP8RT_E4M3)

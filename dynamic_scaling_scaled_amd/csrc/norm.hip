@@ -143,6 +143,7 @@ __global__ void __launch_bounds__(1024) k_rmsnorm_quantize(NormArgs a, RowShape 
     const bool on = row < a.rows;
     if (!kHold) load(row);
     float h[NV][8];
+    uint32_t om[NV];  // max |h w| of each octet
     float ss = 0.0f;
     uint32_t m = 0;
 #pragma unroll
@@ -165,12 +166,15 @@ __global__ void __launch_bounds__(1024) k_rmsnorm_quantize(NormArgs a, RowShape 
       const int o = v * per + tr;
       const bool in = o < octets;
       if (hp && in && on) store8(hp + row * a.ldh + o * 8, h[v]);
+      om[v] = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         ss += h[v][i] * h[v][i];
         h[v][i] *= w[v][i];  // from here on h * w
-        m = max(m, in ? __float_as_uint(h[v][i]) & kAbsMask : 0u);
+        om[v] = max(om[v], __float_as_uint(h[v][i]) & kAbsMask);
       }
+      if (!in) om[v] = 0;  // (0 * a weight that is not finite)
+      m = max(m, om[v]);
     }
     row_sum_max(ss, m, sh[round], L);
     const float rstd = 1.0f / sqrtf(ss * inv_cols + a.norm_eps);
@@ -196,15 +200,11 @@ __global__ void __launch_bounds__(1024) k_rmsnorm_quantize(NormArgs a, RowShape 
     for (int v = 0; v < NV; ++v) {
       const int o = v * per + tr;
       const bool in = o < octets && on;
-      float y[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = h[v][i] * rstd;
       if (seg) {
-        uint32_t gm = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) gm = max(gm, in ? __float_as_uint(y[i]) & kAbsMask : 0u);
+        uint32_t gm = om[v];
         for (int d = seg >> 1; d >= 1; d >>= 1)
           gm = max(gm, static_cast<uint32_t>(__shfl_xor(static_cast<int>(gm), d)));
+        gm = __float_as_uint(__uint_as_float(gm) * rstd) & kAbsMask;  // = max |y|, as for a row
         const int64_t g = in ? row * ng + o / seg : 0;
         const bool lead = in && (o & (seg - 1)) == 0;
         if (a.mode == FP8RT_DYNAMIC) {
@@ -218,11 +218,17 @@ __global__ void __launch_bounds__(1024) k_rmsnorm_quantize(NormArgs a, RowShape 
         }
         if (a.amax_out && lead) a.amax_out[g] = __uint_as_float(gm);
       }
-      if (in) {
-        const u32x2 c = u32x2{cvt4_nan<F>(y[0] * r, y[1] * r, y[2] * r, y[3] * r),
-                              cvt4_nan<F>(y[4] * r, y[5] * r, y[6] * r, y[7] * r)};
-        *reinterpret_cast<u32x2*>(a.q + row * a.ldq + o * 8) = c;
+      float y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = h[v][i] * rstd * r;
+      u32x2 c;
+      if (a.mode == FP8RT_DYNAMIC) {  // a value that is not finite has made r NaN, and all codes with it
+        c = u32x2{cvt4<F>(y[0], y[1], y[2], y[3]), cvt4<F>(y[4], y[5], y[6], y[7])};
+        if (__builtin_isnan(r)) c = u32x2{0x7F7F7F7Fu, 0x7F7F7F7Fu};
+      } else {
+        c = u32x2{cvt4_nan<F>(y[0], y[1], y[2], y[3]), cvt4_nan<F>(y[4], y[5], y[6], y[7])};
       }
+      if (in) *reinterpret_cast<u32x2*>(a.q + row * a.ldq + o * 8) = c;
     }
   }
   if (part) {
