@@ -704,8 +704,8 @@ fp8rt_status fp8_paged_attention(const void* q, fp8rt_dtype qt, int64_t tokens, 
     return FP8RT_EINVAL;
   if (ldq < 0 || hdq < 0 || ldy < 0 || hdy < 0) return FP8RT_EINVAL;
   if (qt != FP8RT_BF16 || yt != FP8RT_BF16) return FP8RT_EUNSUPPORTED;  // activations stay BF16
-  // a workgroup of 256 threads for every 128 query rows of every sequence and head: below 2^31 threads
-  if (seqs * ceil_div(a.p.max_new * (q_heads / heads), 128) * heads > (int64_t(1) << 23)) return FP8RT_EUNSUPPORTED;
+  // a workgroup of up to 512 threads for every 128 query rows of every sequence and head: at most 2^31 threads
+  if (seqs * ceil_div(a.p.max_new * (q_heads / heads), 128) * heads > (int64_t(1) << 22)) return FP8RT_EUNSUPPORTED;
   if (ldq % 8 != 0 || hdq % 8 != 0 || ldy % 4 != 0 || hdy % 4 != 0) return FP8RT_EALIGN;
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned4(k_scale) || !aligned4(v_scale) ||
       (reinterpret_cast<uintptr_t>(y) & 7u) || (lse && !aligned4(lse)))

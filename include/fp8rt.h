@@ -550,7 +550,7 @@ fp8rt_status fp8_kv_append(const void* k, const void* v, fp8rt_dtype xt, int64_t
  *   max_kv : a bound on kv_len (host), used to choose how the work is split; longer
  *            sequences are still computed
  * The scales are those fp8_kv_append writes: positive, or NaN.
- * q_heads a multiple of heads; sm_scale finite; window >= 0; at most 2^23 tiles of
+ * q_heads a multiple of heads; sm_scale finite; window >= 0; at most 2^22 tiles of
  * 128 (token, head of a group) rows over all sequences and heads (else FP8RT_EUNSUPPORTED).
  * Alignment: ldq, hdq multiples of 8, ldy, hdy of 4, q and the caches 16-byte, y 8-byte aligned.
  * Scratch: the per-stream scratch buffer holds the parts of sequences split along their keys. */
