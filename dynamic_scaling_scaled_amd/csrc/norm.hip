@@ -241,8 +241,8 @@ __global__ void __launch_bounds__(1024) k_rmsnorm_quantize(NormArgs a, RowShape 
 
 // ---------------------------------------------------------------------------
 // Gradient.  The same layout; a thread keeps its columns' share of dweight in
-// registers over all its rows.  Rows of one wave (L lanes each) are added at the end,
-// so that a wave (L > 0) or a workgroup (L = 0) writes one share of the row.
+// registers over all its rows; rows side by side (L > 0) are added at the end, so that a
+// workgroup writes one share of dweight.
 template <typename T, typename H, int NV>
 __global__ void __launch_bounds__(1024) k_rmsnorm_backward(NormGradArgs a, RowShape shape, float* dw_part) {
   __shared__ float2 sh[2][kMaxWaves];
@@ -333,18 +333,22 @@ __global__ void __launch_bounds__(1024) k_rmsnorm_backward(NormGradArgs a, RowSh
       }
     }
   }
-  if (dw_part) {
+  if (!dw_part) return;
+  float* share = dw_part + int64_t(blockIdx.x) * a.cols;
+  if (L) {  // (NV = 1, 4 waves, cols <= 512)
+    __shared__ __align__(16) float side[4][512];
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int o = v * per + tr;
-      if (L) {
+    for (int i = 0; i < 8; ++i)
+      for (int d = L; d < 64; d <<= 1) dw[0][i] += __shfl_xor(dw[0][i], d);
+    if ((threadIdx.x & 63) < L && tr < octets) store8(&side[threadIdx.x >> 6][tr * 8], dw[0]);
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.cols; c += 256) share[c] = (side[0][c] + side[1][c]) + (side[2][c] + side[3][c]);
+    return;
+  }
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          for (int d = L; d < 64; d <<= 1) dw[v][i] += __shfl_xor(dw[v][i], d);
-      }
-      const int64_t at = L ? int64_t(blockIdx.x) * (blockDim.x >> 6) + (threadIdx.x >> 6) : blockIdx.x;
-      if (o < octets && (!L || (threadIdx.x & 63) < L)) store8(dw_part + at * a.cols + o * 8, dw[v]);
-    }
+  for (int v = 0; v < NV; ++v) {
+    const int o = v * per + tr;
+    if (o < octets) store8(share + o * 8, dw[v]);
   }
 }
 
@@ -373,12 +377,12 @@ __global__ void __launch_bounds__(256) k_dweight_sum(const float* part, int n, i
 }
 
 // The layout of rows over threads.
-//  - Up to 256 columns: a power of two of lanes a row, several rows a wave.
+//  - Up to 512 columns: a power of two of lanes a row, several rows a workgroup.
 //  - Few rows (under 2 a CU): one octet a thread, the shortest chain.
 //  - Many rows: nv_many octets a thread, looped over by threads_per_cu threads a CU.  Measured at
 //    4096 x 8192 bf16 with residual, us for 1 / 2 / 4 octets: forward 59 / 49 / 74 with 1024 threads a
-//    CU, 61 / 49 / 80 with 2048; gradient 53 / 98 / 256 (dweight's sums spill from 2 on) and
-//    56 / 107 / 280.  One workgroup a row, no loop: 69 and 65.
+//    CU, 61 / 49 / 80 with 2048; gradient 53 / 101 / 302 (dweight's sums spill from 2 on) with 512,
+//    56 / 107 / 280 with 2048.  One workgroup a row, no loop: 69 and 65.
 struct Launch {
   RowShape shape;
   int nv, threads;
@@ -387,7 +391,7 @@ struct Launch {
 Launch shape_for(int64_t rows, int64_t cols, int nv_many, int threads_per_cu) {
   const int64_t octets = cols >> 3;
   Launch g;
-  if (octets <= 32) {
+  if (octets <= 64) {
     int L = 2;
     while (L < octets) L <<= 1;
     g.nv = 1;
@@ -436,8 +440,8 @@ hipError_t launch_rmsnorm_quantize(const NormArgs& a, hipStream_t st) {
 }
 
 hipError_t launch_rmsnorm_backward(const NormGradArgs& a, hipStream_t st) {
-  const Launch g = shape_for(a.rows, a.cols, 1, 1024);
-  const int shares = static_cast<int>(g.shape.L ? g.grid * (g.threads / 64) : g.grid);
+  const Launch g = shape_for(a.rows, a.cols, 1, 512);  // (each workgroup costs a share of dweight)
+  const int shares = static_cast<int>(g.grid);
   void* part = nullptr;
   if (a.dw) {
     const hipError_t e = get_scratch(st, size_t(shares) * a.cols * sizeof(float), &part);

@@ -879,60 +879,67 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs a, Cut cut, P
 }
 
 // ---------------------------------------------------------------------------
-// Adds the chunks of one query row: with M = max m_i,
-// y = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.  A workgroup takes one row,
-// D / 4 threads a chunk, so that 8 (D = 128) or 16 chunks are read at once: the kernel is a chain of
-// loads, and its length is what it costs.
+// Adds the chunks of a query row: with M = max m_i,
+// y = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.  D / 4 threads take a chunk, `lanes` (a power of
+// two, at most the 256 / (D / 4) chunks that a workgroup reads at once) groups of them a row, and a
+// workgroup as many rows as that leaves room for: the kernel is a chain of loads, and its length is what it costs.
 template <int D>
-__global__ void __launch_bounds__(256) k_attend_join(AttendArgs a, Cut cut, int32_t tile_rows, Parts parts) {
+__global__ void __launch_bounds__(256)
+    k_attend_join(AttendArgs a, Cut cut, int32_t tile_rows, int32_t lanes, int32_t rows_total, Parts parts) {
   constexpr int T = D / 4, G = 256 / T;  // threads of a chunk, chunks at once
   __shared__ __align__(16) f32x4 sh_y[G][T];
   __shared__ float2 sh_ml[G];
-  const int x = threadIdx.x % T, y = threadIdx.x / T;
+  const int x = threadIdx.x % T, y = threadIdx.x / T, part = y & (lanes - 1);
   const int32_t group = static_cast<int32_t>(cut.by_group.d);
-  const uint32_t per = static_cast<uint32_t>(a.p.max_new) * cut.by_heads.d;  // by_heads: of the queries here
-  const int64_t b = blockIdx.x / per;
-  const uint32_t rest = blockIdx.x - static_cast<uint32_t>(b) * per;
-  const int32_t i = cut.by_heads.div(rest), h = rest - i * cut.by_heads.d;
-  const SeqSpan s = seq_span(a.p, b);
-  if (i >= s.n) return;
-  const int32_t hg = h - static_cast<int32_t>(cut.by_group.div(h)) * group;
-  const int32_t r0 = (i * group + hg) & ~(tile_rows - 1);
-  const int64_t left = int64_t(s.n) * group - r0;
-  const Range tile = tile_range(a, s, r0, left < tile_rows ? static_cast<int32_t>(left) : tile_rows, cut.by_group);
-  int32_t n = (int64_t(tile.hi) - tile.lo + cut.len - 1) / cut.len;
-  n = n < 1 ? 1 : n > cut.chunks ? cut.chunks : n;
-  const int64_t row = (s.tok0 + i) * a.q_heads + h, step = a.p.tokens * a.q_heads;
+  const uint32_t r = blockIdx.x * (G / lanes) + y / lanes;  // (sequence, token, query head)
+  const uint32_t rt = cut.by_heads.div(r);                  // by_heads: of the queries here
+  const int32_t h = r - rt * cut.by_heads.d;
+  const int64_t b = cut.by_tiles.div(rt);                   // by_tiles: max_new here
+  const int32_t i = rt - static_cast<uint32_t>(b) * cut.by_tiles.d;
+  bool on = r < static_cast<uint32_t>(rows_total);
   float m = kNoKey, l = 0.0f;
   f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+  int64_t tok = 0;
+  if (on) {
+    const SeqSpan s = seq_span(a.p, b);
+    on = i < s.n;
+    if (on) {
+      tok = s.tok0 + i;
+      const int32_t hg = h - static_cast<int32_t>(cut.by_group.div(h)) * group;
+      const int32_t r0 = (i * group + hg) & ~(tile_rows - 1);
+      const int64_t left = int64_t(s.n) * group - r0;
+      const Range tile = tile_range(a, s, r0, left < tile_rows ? static_cast<int32_t>(left) : tile_rows, cut.by_group);
+      int32_t n = (int64_t(tile.hi) - tile.lo + cut.len - 1) / cut.len;
+      n = n < 1 ? 1 : n > cut.chunks ? cut.chunks : n;
+      const int64_t row = tok * a.q_heads + h, step = a.p.tokens * a.q_heads;
 #pragma unroll 4
-  for (int32_t k = y; k < n; k += G) {
-    const float2 ml = parts.ml[k * step + row];
-    const f32x4 v = *reinterpret_cast<const f32x4*>(parts.o + (k * step + row) * D + 4 * x);
-    const float mn = fmaxf(m, ml.x), fa = exp2_fast(m - mn), fb = exp2_fast(ml.x - mn);
-    l = l * fa + ml.y * fb;
-    o = o * fa + v * fb;
-    m = mn;
+      for (int32_t k = part; k < n; k += lanes) {
+        const float2 ml = parts.ml[k * step + row];
+        const f32x4 v = *reinterpret_cast<const f32x4*>(parts.o + (k * step + row) * D + 4 * x);
+        const float mn = fmaxf(m, ml.x), fa = exp2_fast(m - mn), fb = exp2_fast(ml.x - mn);
+        l = l * fa + ml.y * fb;
+        o = o * fa + v * fb;
+        m = mn;
+      }
+    }
   }
   sh_y[y][x] = o;
   if (x == 0) sh_ml[y] = make_float2(m, l);
   __syncthreads();
-  if (y != 0) return;
+  if (!on || part != 0) return;
   float base = kNoKey;
-#pragma unroll
-  for (int k = 0; k < G; ++k) base = fmaxf(base, sh_ml[k].x);
+  for (int k = 0; k < lanes; ++k) base = fmaxf(base, sh_ml[y + k].x);
   l = 0.0f;
   o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int k = 0; k < G; ++k) {
-    const float f = exp2_fast(sh_ml[k].x - base);
-    l += sh_ml[k].y * f;
-    o += sh_y[k][x] * f;
+  for (int k = 0; k < lanes; ++k) {
+    const float f = exp2_fast(sh_ml[y + k].x - base);
+    l += sh_ml[y + k].y * f;
+    o += sh_y[y + k][x] * f;
   }
   const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-  *reinterpret_cast<u32x2*>(a.y + (s.tok0 + i) * a.ldy + h * a.hdy + 4 * x) =
+  *reinterpret_cast<u32x2*>(a.y + tok * a.ldy + h * a.hdy + 4 * x) =
       u32x2{pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
-  if (a.lse && x == 0) a.lse[row] = l != 0.0f ? (base + log2_fast(l)) * kLn2 : -INFINITY;
+  if (a.lse && x == 0) a.lse[tok * a.q_heads + h] = l != 0.0f ? (base + log2_fast(l)) * kLn2 : -INFINITY;
 }
 
 }  // namespace
@@ -944,20 +951,21 @@ hipError_t launch_paged_attention(const AttendArgs& a, hipStream_t st) {
   const int64_t tile_rows = few ? 16 : 128;
   const int64_t tiles = ceil_div(rows, tile_rows);
   const int64_t jobs = a.p.seqs * tiles * a.p.heads;  // workgroups without a cut
-  // Cut the keys when the jobs alone do not fill the card.  Prompts: to the 2
-  // workgroups that a CU holds.  Decode (1 a CU): a long stream per workgroup costs least (two
-  // sequences of 131072 tokens, 8 heads: 92 us in 256 chunks, 101 in 2048, and the parts' addition
-  // 5 and 7 us), so 1 a CU, and 2 from 8 sequences on, whose ragged lengths then even out; chunks of at least
-  // 1024 keys, below which a second launch costs more than the first saves (1001 keys: 10.6 us uncut,
-  // 8.6 + 3.9 in halves).  A window bounds what a causal tile can see.
+  // Cut the keys when the jobs alone do not fill the card.  Prompts: when they leave
+  // half of the 2 workgroups that a CU holds free.  Decode (1 a CU): a long stream per workgroup costs
+  // least (two sequences of 131072 tokens, 8 heads: 92 us in 256 chunks, 101 in 2048, and the parts'
+  // addition 5 and 7 us), so 1 a CU, and 2 from 8 sequences on, whose ragged lengths then even out; chunks of at
+  // least 1024 keys, below which the second launch costs more than the cut saves (1001 keys: 10.6 us
+  // uncut, 8.6 + 3.9 in halves).  Prompts' steps of 64 keys take 2 us each, so theirs may be shorter:
+  // 512 keys, 256 where they leave most CUs idle.  A window bounds what a causal tile can see.
   Cut cut;
   cut.chunks = 1;
   cut.len = 64;
   int64_t span = a.max_kv;
   if (a.causal && a.window > 0) span = std::min(span, a.window + tile_rows / group + 64);
   const int64_t want = ceil_div(int64_t(few && a.p.seqs < 8 ? 1 : 2) * device_cus(), jobs);
-  if (want > 1) {
-    const int64_t len = std::max<int64_t>(few ? 1024 : 512, ceil_div(ceil_div(span, want), 64) * 64);
+  if (few ? want > 1 : jobs <= device_cus()) {
+    const int64_t len = std::max<int64_t>(few ? 1024 : 4 * jobs > device_cus() ? 512 : 256, ceil_div(ceil_div(span, want), 64) * 64);
     cut.chunks = static_cast<int32_t>(ceil_div(span, len));
     cut.len = static_cast<int32_t>(len);
   }
@@ -991,9 +999,13 @@ hipError_t launch_paged_attention(const AttendArgs& a, hipStream_t st) {
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && cut.chunks > 1) {
     cut.by_heads = FastDiv(static_cast<uint32_t>(a.q_heads));
-    const dim3 jg(static_cast<uint32_t>(a.p.seqs * a.p.max_new * a.q_heads));
+    cut.by_tiles = FastDiv(static_cast<uint32_t>(a.p.max_new));
+    const int32_t all = static_cast<int32_t>(a.p.seqs * a.p.max_new * a.q_heads), at_once = 1024 / a.p.dim;
+    int32_t lanes = 1;
+    while (lanes < at_once && lanes < cut.chunks) lanes <<= 1;
+    const dim3 jg(static_cast<uint32_t>(ceil_div(all, at_once / lanes)));
     auto join = [&](auto kern) {
-      hipLaunchKernelGGL(kern, jg, dim3(256), 0, st, a, cut, static_cast<int32_t>(tile_rows), parts);
+      hipLaunchKernelGGL(kern, jg, dim3(256), 0, st, a, cut, static_cast<int32_t>(tile_rows), lanes, all, parts);
     };
     a.p.dim == 128 ? join(k_attend_join<128>) : join(k_attend_join<64>);
     e = hipGetLastError();
