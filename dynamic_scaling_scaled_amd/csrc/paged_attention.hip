@@ -107,6 +107,11 @@ __device__ __forceinline__ int hidden_zero() {
 // Keeps the compiler from moving instructions across this point: the kernels' loops
 // say themselves which work runs under which matrix instruction.
 __device__ __forceinline__ void pin() { __builtin_amdgcn_sched_barrier(0); }
+// This wave's priority among those of its SIMD.  A tile starts urgent and gets less so: the
+// two waves of a SIMD drift apart, one feeding the matrix cores while the other widens and waits
+// (8192-token prompt, 64 / 8 heads of 128: 1086 us, without 1130, urgent throughout 1227).
+template <int P>
+__device__ __forceinline__ void urgent() { __builtin_amdgcn_s_setprio(P); }
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float log2_fast(float x) { return __builtin_amdgcn_logf(x); }
 
@@ -138,6 +143,7 @@ __device__ __forceinline__ Range tile_range(const AttendArgs& a, const SeqSpan& 
 // start is dependent loads and index arithmetic, which the 64-bit quotients dominated.
 struct Cut {
   int32_t chunks, len;
+  int32_t ordered;  // decode: the longest of at most 64 sequences first
   FastDiv by_heads, by_tiles, by_chunks, by_group;
 };
 
@@ -161,6 +167,19 @@ __device__ __forceinline__ Range chunk_of(const Range& t, const Cut& c, int32_t 
   const int64_t lo = int64_t(t.lo) + int64_t(i) * c.len, hi = lo + c.len;
   return Range{lo < t.hi ? static_cast<int32_t>(lo) : t.hi,
                i == c.chunks - 1 || hi > t.hi ? t.hi : static_cast<int32_t>(hi)};
+}
+
+// The sequence of rank `slot` by falling length, of at most 64 (one a lane).  Where workgroups
+// outnumber the places on the card, the long ones must not start last.
+__device__ __forceinline__ int32_t by_length(const PagedArgs& p, int32_t slot) {
+  const int32_t lane = threadIdx.x & 63, n = static_cast<int32_t>(p.seqs);
+  const int32_t len = p.kv_len[lane < n ? lane : 0];
+  int32_t rank = 0;
+  for (int32_t j = 0; j < n; ++j) {
+    const int32_t other = __builtin_amdgcn_readlane(len, j);
+    rank += other > len || (other == len && j < lane);
+  }
+  return __builtin_ctzll(__ballot(lane < n && rank == slot));
 }
 
 // Partial results of cut tiles, in the stream's scratch.
@@ -286,7 +305,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) k_attend_few(AttendArgs a, Cut
   const int32_t heads = a.p.heads, group = static_cast<int32_t>(cut.by_group.d);
   const Place place = place_of(blockIdx.x, cut);
   const int32_t head = place.head, chunk = place.chunk, r0 = place.tile * 16;
-  const int64_t b = place.b;
+  const int64_t b = cut.ordered ? by_length(a.p, place.b) : static_cast<int32_t>(place.b);
   const SeqSpan s = seq_span(a.p, b);
   const int64_t all = int64_t(s.n) * group;
   if (r0 >= all) return;
@@ -547,9 +566,10 @@ __device__ __forceinline__ u32x2 read_tr(const uint8_t* p) {
   return __builtin_bit_cast(u32x2, v);
 }
 
-template <int F, int D>
-__global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs a, Cut cut, Parts parts) {
-  constexpr int NP = D / 64;   // 16-byte pieces of keys, and of values, that a thread stages
+template <int F, int D, int NW>
+__global__ void __launch_bounds__(64 * NW, 2) k_attend_many(AttendArgs a, Cut cut, Parts parts) {
+  constexpr int NP = D / (16 * NW);  // 16-byte pieces of keys, and of values, that a thread stages
+  constexpr int WG = 32 * NW;        // query rows
   constexpr int KS = D / 16;   // matrix steps along the dimensions
   constexpr int DT = D / 32;   // 32-wide output tiles
   constexpr int kBuf = kBK * D * 2;  // bytes of one buffer of keys, and of values
@@ -561,12 +581,12 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs a, Cut cut, P
   const int32_t heads = a.p.heads, group = static_cast<int32_t>(cut.by_group.d);
   const Place place = place_of(blockIdx.x, cut);
   const int32_t head = place.head, chunk = place.chunk;
-  const int32_t r0 = (cut.by_tiles.d - 1 - place.tile) * 128;  // causal: the longest first
+  const int32_t r0 = (cut.by_tiles.d - 1 - place.tile) * WG;  // causal: the longest first
   const int64_t b = place.b;
   const SeqSpan s = seq_span(a.p, b);
   const int64_t all = int64_t(s.n) * group;
   if (r0 >= all) return;
-  const int32_t rows = all - r0 < 128 ? static_cast<int32_t>(all - r0) : 128;
+  const int32_t rows = all - r0 < WG ? static_cast<int32_t>(all - r0) : WG;
   const Range tile = tile_range(a, s, r0, rows, cut.by_group);
   const Range part = chunk_of(tile, cut, chunk);
   if (chunk > 0 && part.lo >= part.hi) return;
@@ -617,8 +637,9 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs a, Cut cut, P
   constexpr int WK = 64 / TK;          // keys of a wave's piece
   const int sk = threadIdx.x / TK, sp = threadIdx.x % TK;
   const uint32_t lane_at = (lane / TK) * D + 16 * sp;
-  const int mine = NP == 2 ? wave & 1 : 0;                            // the piece whose part's scales this wave takes
-  const int mine_part = NP == 2 ? (wave >> 1) + 2 * (wave & 1) : wave;
+  // the piece whose part's scales this wave takes, and the part (16 keys are one or two waves' pieces)
+  const int mine = NP == 2 ? wave & 1 : 0;
+  const int mine_part = NP == 2 ? (wave >> 1) + 2 * (wave & 1) : WK == 16 ? wave : wave >> 1;
   // looked up by vector loads, which retire in order with the tiles' (a scalar load
   // would make every wait for an LDS read wait for it too)
   const int32_t* table = a.p.table + b * a.p.ld_table + hidden_zero();
@@ -801,6 +822,7 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs a, Cut cut, P
 #pragma unroll
       for (int e = 0; e < 4; ++e) ps[e] = sh_p[buf][e];
       pin();
+      urgent<2>();
       scores(0, [&](int i) {
         if (i == KS - 1) ahead_k(1);
       });
@@ -815,6 +837,7 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs a, Cut cut, P
         redo |= sh_odd[buf] == t;
         hide(0);
       }
+      urgent<1>();
       scores(1, [&](int i) {
         weigh(0, 16 / KS * i, 16 / KS);
         if (i == KS - 1) ahead_v(0);
@@ -825,6 +848,7 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs a, Cut cut, P
         weigh(1, 16 / (2 * DT) * i, 16 / (2 * DT));
         if (i == 2 * DT - 1) ahead_v(1);
       });
+      urgent<0>();
       follow(1);
       if (more) {
         repair(buf ^ 1, t + 1);
@@ -948,7 +972,8 @@ hipError_t launch_paged_attention(const AttendArgs& a, hipStream_t st) {
   const int64_t group = a.q_heads / a.p.heads;
   const int64_t rows = a.p.max_new * group;
   const bool few = rows <= 16;
-  const int64_t tile_rows = few ? 16 : 128;
+  const bool wide = !few && a.p.dim == 128 && a.p.seqs * (rows / 256) * a.p.heads >= 2 * device_cus();
+  const int64_t tile_rows = few ? 16 : wide ? 256 : 128;
   const int64_t tiles = ceil_div(rows, tile_rows);
   const int64_t jobs = a.p.seqs * tiles * a.p.heads;  // workgroups without a cut
   // Cut the keys when the jobs alone do not fill the card.  Prompts: when they leave
@@ -969,6 +994,7 @@ hipError_t launch_paged_attention(const AttendArgs& a, hipStream_t st) {
     cut.chunks = static_cast<int32_t>(ceil_div(span, len));
     cut.len = static_cast<int32_t>(len);
   }
+  cut.ordered = few && cut.chunks == 1 && jobs > device_cus() && a.p.seqs <= 64;
   Parts parts{nullptr, nullptr};
   if (cut.chunks > 1) {
     const size_t n = size_t(cut.chunks) * a.p.tokens * a.q_heads;
@@ -983,14 +1009,14 @@ hipError_t launch_paged_attention(const AttendArgs& a, hipStream_t st) {
   cut.by_tiles = FastDiv(static_cast<uint32_t>(tiles));
   cut.by_chunks = FastDiv(cut.chunks);
   cut.by_group = FastDiv(static_cast<uint32_t>(group));
-  const int waves = few ? kFewWaves : 4;
+  const int waves = few || wide ? 8 : 4;
   auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(grid), dim3(64 * waves), 0, st, a, cut, parts); };
   auto by_dim = [&](auto f) {
     constexpr int F = decltype(f)::value;
     if (few)
       a.p.dim == 128 ? go(k_attend_few<F, 128>) : go(k_attend_few<F, 64>);
     else
-      a.p.dim == 128 ? go(k_attend_many<F, 128>) : go(k_attend_many<F, 64>);
+      wide ? go(k_attend_many<F, 128, 8>) : a.p.dim == 128 ? go(k_attend_many<F, 128, 4>) : go(k_attend_many<F, 64, 4>);
   };
   if (a.p.fmt == FP8RT_E4M3)
     by_dim(std::integral_constant<int, kE4M3>{});

@@ -116,6 +116,27 @@ def test_longer_prompt(rt):
     run(rt, ref.Batch([300], [130], 64), 1, 4, 128, fmt=1)
 
 
+@pytest.mark.parametrize("causal,window,fmt", [(True, 0, 0), (True, 37, 1), (False, 0, 0)])
+def test_many_rows(rt, causal, window, fmt):
+    """Enough (token, head) rows for the widest workgroups, ragged, with a missing page and values that are
+    not finite where some rows see them."""
+    bt = ref.Batch([64] * 15 + [50], [(37 * i) % 90 for i in range(16)], 16)
+    bt.table[3, 2] = -1
+    kc, vc, ks, vs = make(bt, 8, 128, fmt, 21)
+    vc[int(bt.table[5, bt.lens[5] // 16 - 1]), 1, 3, 7] = 0x7F
+    vs[int(bt.table[6, 1]), 2] = math.nan
+    run(rt, bt, 8, 16, 128, fmt, causal=causal, window=window, kv=(kc, vc, ks, vs))
+
+
+@pytest.mark.parametrize("seqs", [40, 64, 70])
+def test_many_sequences(rt, seqs):
+    """More (sequence, head) pairs than CUs: the longest go first, equal and empty ones among them."""
+    before = [(61 * i) % 157 if i % 3 else 64 for i in range(seqs)]
+    before[5], before[7], before[11] = -1, -1, 700
+    run(rt, ref.Batch([1] * seqs, before, 16), 8, 2, 64)
+    run(rt, ref.Batch([2] * seqs, before, 32), 8, 1, 128, window=50)
+
+
 def test_long_context(rt):
     run(rt, ref.Batch([1, 1, 2], [9000, 20, 4000], 64), 2, 8, 128)
     run(rt, ref.Batch([1], [9000], 16), 1, 4, 64, window=5000)
