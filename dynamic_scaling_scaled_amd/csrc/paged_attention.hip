@@ -3,7 +3,7 @@
 //
 // Mathematics.  With t_j = z_j log2(e) the scores of the visible positions and
 // v_j = s_j dec(code_j) their values (s_j the page's v scale), the weight
-//   w_j = 2^(t_j + log2 s_j - m),   m at most 15 below max_j (t_j + log2 s_j),
+//   w_j = 2^(t_j + log2 s_j - m),   m at most 15 below the maximum of t_j + log2 s_j,
 // turns the output into  y = sum_j w_j dec(code_j) / sum_j (w_j / s_j):  the codes go
 // into the second matrix product as they are, the weights stay within
 // fp16 whatever the pages' scales, and the sums follow in one pass over the keys
@@ -23,7 +23,7 @@
 // A query row is a (token, head of the group) pair: row r of a sequence and
 // key / value head is token r / group, head r % group, so the heads that share keys share
 // their loads.  Two kernels: k_attend_few for up to 16 rows (decode), each wave streaming its own
-// keys from HBM; k_attend_many, 128 rows a workgroup, keys and values staged in LDS.
+// keys from HBM; k_attend_many, 128 or 256 rows a workgroup, keys and values staged in LDS.
 // Long key ranges are cut into chunks, whose unnormalised sums k_attend_join adds.
 #include <algorithm>
 #include <type_traits>
@@ -281,11 +281,14 @@ __device__ void careful_store(const AttendArgs& a, const Parts& parts, int32_t c
 
 // ---------------------------------------------------------------------------
 // Up to 16 query rows: decode.  A workgroup takes one tile of 16 rows and one
-// chunk of keys; its waves take 32-key steps in turn, each with its own
-// running maximum and sums, joined through LDS at the end.  The keys of a
-// step go from HBM to registers in operand order: lane l (c = l % 16, g = l / 16)
-// loads 16-byte pieces of key c of each 16-key part, and for the keys
-// {4g..4g+3, 16+4g..16+4g+3}, whose scores it will hold, D/16 bytes of the values.
+// chunk of keys; its waves take 32-key steps in turn, each with its own reference and sums,
+// joined through LDS at the end.  The keys of a step go from HBM to registers in operand order:
+// lane l (c = l % 16, g = l / 16) loads 16-byte pieces of key c of each 16-key part, and for the keys
+// {4g..4g+3, 16+4g..16+4g+3}, whose scores it will hold, D/16 bytes of the values; byte b of every
+// key's dword w makes output tile 4w + b, so that two byte permutes a pair of codes transpose them.
+// Bound by reading the codes: two sequences of 131072 tokens, 8 heads of 128, 90 us (6.0 TB/s, what a
+// read-only pass reaches) and 5 us for the join; 64 ragged sequences of up to 8191 102 us (5.4 TB/s: the
+// last workgroups end apart); one of 1001 tokens 11 us, a chain of launch, plan, table and 4 steps.
 // 8 waves a workgroup: 64 ragged sequences of up to 8192 tokens, 8 heads, in one piece each,
 // 114 us; 4 waves 124; 16 (which no longer fit the registers) 166.
 constexpr int kFewWaves = 8;
@@ -541,12 +544,19 @@ __global__ void __launch_bounds__(64 * kFewWaves) k_attend_few(AttendArgs a, Cut
 }
 
 // ---------------------------------------------------------------------------
-// 128 query rows a workgroup, 32 a wave: prompts and chunks of prompts.  Tiles of 64 keys
+// 32 query rows a wave, 4 or 8 waves a workgroup: prompts and chunks of prompts.  Tiles of 64 keys
 // are widened once into LDS (keys to bf16, values to fp16) while the tile before is computed
 // from the other buffer, one barrier a tile.  Rows of 2 D bytes are
 // stored with their 16-byte (keys) or 64-byte (values) pieces permuted by the key, so that the
 // operand reads -- 16 bytes of 16 keys; 8 bytes of 4 keys, transposed by ds_read_b64_tr_b16 --
 // touch every bank once.
+// Bound by issue: a tile and wave are 32 matrix instructions (1024 cycles), about 235 vector
+// instructions, 32 exponentials among them (1080 cycles), and LDS reads that a CU's waves
+// share (a wave's 32 rows use each operand once).  Matrix cores busy 45% of the time, vector units 47%.  64 rows
+// a wave would halve the LDS reads, but leave one wave a SIMD and move accumulators between register
+// files: 1666 us against 1288 then.  8 waves share a tile's widening: 1131 us against 1228 with 4.
+// An 8192-token prompt, 64 heads over 8 of 128: 1086 to 1115 us, 1.0 PFLOP/s, where a bf16 library
+// product of 8192^3 reaches 1.19 on the same card.
 constexpr int kBK = 64;
 
 template <int D>
@@ -906,7 +916,8 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attend_many(AttendArgs a, Cut cu
 // Adds the chunks of a query row: with M = max m_i,
 // y = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.  D / 4 threads take a chunk, `lanes` (a power of
 // two, at most the 256 / (D / 4) chunks that a workgroup reads at once) groups of them a row, and a
-// workgroup as many rows as that leaves room for: the kernel is a chain of loads, and its length is what it costs.
+// workgroup as many rows as that leaves room for: the kernel is a chain of loads, and its length is
+// what it costs (32 chunks of 128 rows: 5 us; one wave a row took 10 to 29).
 template <int D>
 __global__ void __launch_bounds__(256)
     k_attend_join(AttendArgs a, Cut cut, int32_t tile_rows, int32_t lanes, int32_t rows_total, Parts parts) {

@@ -21,7 +21,8 @@
  *        + ceil(N/256)) * K/128 * 1024 bytes) and transposed 1x128 A scales
  *        (ceil(M/256) * 256 * K/128 * 4 bytes), the FP32 parts of a last wave
  *        split along K (up to 4 parts x 256 KB per split 256 x 256 tile), the
- *        cast-transpose's per-group arrays and the ledger's partials.  When a
+ *        cast-transpose's per-group arrays, the ledger's partials, the shares of
+ *        a norm's weight gradient and the parts of attention cut along its keys.  When a
  *        call needs more, a larger buffer (at least twice the old) is
  *        allocated and the old one is KEPT, never freed: every address handed
  *        to a kernel stays valid for the process's life.
@@ -486,7 +487,7 @@ fp8rt_status fp8_rmsnorm_quantize(const void* x, fp8rt_dtype xt, int64_t rows, i
  * Alignment: cols and leading dimensions multiples of 16, matrices, weight and
  * dweight 16-byte aligned, cols <= 32768 (else FP8RT_EUNSUPPORTED).
  * Scratch: the per-stream scratch buffer holds the dweight partials (at most
- * 512 x cols floats). */
+ * 4 x cols floats per CU). */
 fp8rt_status fp8_rmsnorm_backward(const void* dy, fp8rt_dtype dyt, int64_t rows, int64_t cols, int64_t lddy,
                                   const void* h, fp8rt_dtype ht, int64_t ldh, const void* weight, fp8rt_dtype wt,
                                   const float* rstd, const void* dresidual, int64_t lddr, void* dx, int64_t lddx,
@@ -553,7 +554,9 @@ fp8rt_status fp8_kv_append(const void* k, const void* v, fp8rt_dtype xt, int64_t
  * q_heads a multiple of heads; sm_scale finite; window >= 0; at most 2^22 tiles of
  * 128 (token, head of a group) rows over all sequences and heads (else FP8RT_EUNSUPPORTED).
  * Alignment: ldq, hdq multiples of 8, ldy, hdy of 4, q and the caches 16-byte, y 8-byte aligned.
- * Scratch: the per-stream scratch buffer holds the parts of sequences split along their keys. */
+ * Scratch: the per-stream scratch buffer holds the parts of key ranges cut into chunks
+ * (chunks x tokens x q_heads x (head_dim + 2) floats; the number of chunks depends on the
+ * host arguments alone, so a warm call with the same bounds never grows it). */
 fp8rt_status fp8_paged_attention(const void* q, fp8rt_dtype qt, int64_t tokens, int64_t q_heads, int64_t ldq,
                                  int64_t hdq, const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale,
                                  const float* v_scale, fp8rt_format f, int64_t pages, int64_t heads,
