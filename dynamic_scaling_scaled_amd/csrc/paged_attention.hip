@@ -987,8 +987,8 @@ hipError_t launch_paged_attention(const AttendArgs& a, hipStream_t st) {
   const int64_t tile_rows = few ? 16 : wide ? 256 : 128;
   const int64_t tiles = ceil_div(rows, tile_rows);
   const int64_t jobs = a.p.seqs * tiles * a.p.heads;  // workgroups without a cut
-  // Cut the keys when the jobs alone do not fill the card.  Prompts: when they leave
-  // half of the 2 workgroups that a CU holds free.  Decode (1 a CU): a long stream per workgroup costs
+  // Cut the keys when the jobs alone do not fill the card.  Prompts: when they leave half of the
+  // workgroups that the CUs hold free.  Decode (1 a CU): a long stream per workgroup costs
   // least (two sequences of 131072 tokens, 8 heads: 92 us in 256 chunks, 101 in 2048, and the parts'
   // addition 5 and 7 us), so 1 a CU, and 2 from 8 sequences on, whose ragged lengths then even out; chunks of at
   // least 1024 keys, below which the second launch costs more than the cut saves (1001 keys: 10.6 us
@@ -996,15 +996,23 @@ hipError_t launch_paged_attention(const AttendArgs& a, hipStream_t st) {
   // 512 keys, 256 where they leave most CUs idle.  A window bounds what a causal tile can see.
   Cut cut;
   cut.chunks = 1;
-  cut.len = 64;
+  cut.len = 0;
   int64_t span = a.max_kv;
   if (a.causal && a.window > 0) span = std::min(span, a.window + tile_rows / group + 64);
-  const int64_t want = ceil_div(int64_t(few && a.p.seqs < 8 ? 1 : 2) * device_cus(), jobs);
-  if (few ? want > 1 : jobs <= device_cus()) {
-    const int64_t len = std::max<int64_t>(few ? 1024 : 4 * jobs > device_cus() ? 512 : 256, ceil_div(ceil_div(span, want), 64) * 64);
-    cut.chunks = static_cast<int32_t>(ceil_div(span, len));
-    cut.len = static_cast<int32_t>(len);
+  const int64_t cus = device_cus();
+  if (few) {
+    const int64_t want = ceil_div((a.p.seqs < 8 ? 1 : 2) * cus, jobs);
+    if (want > 1) cut.len = static_cast<int32_t>(std::max<int64_t>(1024, ceil_div(ceil_div(span, want), 64) * 64));
+  } else {
+    // tiles that the tokens can fill, and workgroups that fit at once (registers)
+    const int64_t busy = std::min(jobs, (a.p.tokens * group / tile_rows + a.p.seqs) * a.p.heads);
+    const int64_t fit = (a.p.dim == 64 ? 3 : 2) * cus;
+    if (2 * busy <= fit)
+      cut.len = static_cast<int32_t>(
+          std::max<int64_t>(4 * busy > cus ? 512 : 256, ceil_div(ceil_div(span, ceil_div(fit, busy)), 64) * 64));
   }
+  if (cut.len > 0) cut.chunks = static_cast<int32_t>(ceil_div(span, cut.len));
+  if (cut.chunks == 1) cut.len = 64;
   cut.ordered = few && cut.chunks == 1 && jobs > device_cus() && a.p.seqs <= 64;
   Parts parts{nullptr, nullptr};
   if (cut.chunks > 1) {
