@@ -565,6 +565,23 @@ fp8rt_status fp8_paged_attention(const void* q, fp8rt_dtype qt, int64_t tokens, 
                                  int64_t max_kv, float sm_scale, int32_t causal, int64_t window, void* y,
                                  fp8rt_dtype yt, int64_t ldy, int64_t hdy, float* lse, hipStream_t stream);
 
+/* The four calls above with their arguments as 64-bit words, for bindings that pay for every
+ * argument they convert (31 arguments through a foreign-function interface can cost more than the
+ * smallest of these kernels).
+ *   words[0]    : the call (fp8rt_call)
+ *   words[1 ..] : its arguments in the order of its declaration: pointers and integers
+ *                 as they are, a granularity as two words, a float as the bits of a binary64
+ *   n           : the number of words, which must be the call's (else FP8RT_EINVAL)
+ * An integer that its parameter's type cannot hold is FP8RT_EINVAL; otherwise the
+ * same call with the same result.  `words` is read before the call returns. */
+typedef FP8RT_ENUM(fp8rt_call) {
+  FP8RT_CALL_RMSNORM_QUANTIZE = 0,
+  FP8RT_CALL_RMSNORM_BACKWARD = 1,
+  FP8RT_CALL_KV_APPEND = 2,
+  FP8RT_CALL_PAGED_ATTENTION = 3
+} fp8rt_call;
+fp8rt_status fp8_call_packed(const int64_t* words, int64_t n);
+
 /* Human-readable name of a status code (static storage). */
 const char* fp8rt_status_string(fp8rt_status s);
 

@@ -134,6 +134,36 @@ def test_attention_refusals(rt, kw, status):
     assert attend(rt, **kw) == getattr(rt, status)
 
 
+def test_packed_call(rt):
+    """Arguments as 64-bit words: the same refusals as the call itself, and its own."""
+    import struct
+
+    L = rt.lib()
+
+    def packed(fmt, *words):
+        record = struct.pack(fmt, *words)
+        return L.fp8_call_packed(record, len(record) // 8)
+
+    def grad(dy=FAKE, rows=8, lddy=256, dyt=1, h=FAKE * 2, call=1, fmt="18q", extra=()):
+        return packed(fmt, call, dy, dyt, rows, 256, lddy, h, 1, 256, FAKE, 1, FAKE, 0, 0, FAKE * 3, 256, FAKE, 0, *extra)
+
+    assert grad(dy=0) == rt.EINVAL and grad(rows=0) == rt.EINVAL and grad(lddy=128) == rt.EINVAL
+    assert grad(lddy=264) == rt.EALIGN and grad(h=FAKE + 8) == rt.EALIGN
+    assert grad(dyt=1 + 2 ** 32) == rt.EINVAL        # an enumerator does not wrap
+    assert grad(call=4) == rt.EINVAL and grad(call=-1) == rt.EINVAL
+    assert grad(call=0) == rt.EINVAL and grad(call=2) == rt.EINVAL  # another call's number of words
+    assert grad(fmt="19q", extra=(0,)) == rt.EINVAL
+    assert L.fp8_call_packed(None, 18) == rt.EINVAL and L.fp8_call_packed(b"", 0) == rt.EINVAL
+
+    def norm(eps=1e-12, norm_eps=1e-6, gr=1, gc=0, mode=0):
+        return packed("10qd4qd10q", 0, FAKE, 1, 8, 256, 256, 0, 0, FAKE, 1,
+                      norm_eps, gr, gc, 0, mode, eps, 0, FAKE, 0, FAKE, 256, 0, 0, 0, 0, 0)
+
+    assert norm(eps=0.0) == rt.EINVAL and norm(norm_eps=-1.0) == rt.EINVAL and norm(mode=7) == rt.EINVAL
+    assert norm(gr=2) == rt.EUNSUPPORTED and norm(gr=0) == rt.EUNSUPPORTED and norm(gc=48) == rt.EUNSUPPORTED
+    assert norm(gr=2 ** 40) == rt.EINVAL
+
+
 def test_binding_refusals(rt):
     """Shapes and types the binding turns down before it passes pointers (CPU tensors: never used)."""
     bf, f32, u8, i32 = torch.bfloat16, torch.float32, torch.uint8, torch.int32
