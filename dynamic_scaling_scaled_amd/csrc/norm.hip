@@ -345,9 +345,9 @@ __global__ void __launch_bounds__(1024) k_rmsnorm_backward(NormGradArgs a, RowSh
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       for (int d = L; d < 64; d <<= 1) dw[0][i] += __shfl_xor(dw[0][i], d);
-    if ((threadIdx.x & 63) < L && tr < octets) store8(&side[threadIdx.x >> 6][tr * 8], dw[0]);
+    if (static_cast<int>(threadIdx.x & 63) < L && tr < octets) store8(&side[threadIdx.x >> 6][tr * 8], dw[0]);
     __syncthreads();
-    for (int c = threadIdx.x; c < a.cols; c += 256) share[c] = (side[0][c] + side[1][c]) + (side[2][c] + side[3][c]);
+    for (int64_t c = threadIdx.x; c < a.cols; c += 256) share[c] = (side[0][c] + side[1][c]) + (side[2][c] + side[3][c]);
     return;
   }
 #pragma unroll

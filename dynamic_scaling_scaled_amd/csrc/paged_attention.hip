@@ -144,6 +144,7 @@ __device__ __forceinline__ Range tile_range(const AttendArgs& a, const SeqSpan& 
 struct Cut {
   int32_t chunks, len;
   int32_t ordered;  // decode: the longest of at most 64 sequences first
+  int32_t mixed;    // both kernels run, each for the sequences that are its own (short: up to 16 rows)
   FastDiv by_heads, by_tiles, by_chunks, by_group;
 };
 
@@ -182,10 +183,12 @@ __device__ __forceinline__ int32_t by_length(const PagedArgs& p, int32_t slot) {
   return __builtin_ctzll(__ballot(lane < n && rank == slot));
 }
 
-// Partial results of cut tiles, in the stream's scratch.
+// Partial results of cut tiles, in the stream's scratch.  Rows: (sequence, head, row of its
+// tile) of k_attend_few, (token, query head) of k_attend_many.
 struct Parts {
-  float* o;    // [chunk][token][q head][D], unnormalised
-  float2* ml;  // [chunk][token][q head]: m, sum of w / s
+  float* o;      // [chunk][row][D], unnormalised
+  float2* ml;    // [chunk][row]: m, sum of w / s
+  int64_t rows;
 };
 
 // What one 16-key part of a step needs from its page: t = dot * c, log2 of the v scale, its inverse.
@@ -259,11 +262,10 @@ __device__ void careful_row(const AttendArgs& a, int64_t b, int32_t head, int64_
 
 // Writes such a row: the output (one chunk) or its part.
 template <int D>
-__device__ void careful_store(const AttendArgs& a, const Parts& parts, int32_t chunks, int32_t chunk, int64_t tok,
+__device__ void careful_store(const AttendArgs& a, const Parts& parts, int32_t chunks, int64_t at, int64_t tok,
                               int64_t qh, float m, float l, const float* y) {
   constexpr int E = D / 64;
   const int lane = threadIdx.x & 63;
-  const int64_t at = (int64_t(chunk) * a.p.tokens + tok) * a.q_heads + qh;
   const float inv = l != 0.0f ? 1.0f / l : 0.0f;
   for (int e = 0; e < E; ++e) {
     if (chunks == 1)
@@ -311,7 +313,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) k_attend_few(AttendArgs a, Cut
   const int64_t b = cut.ordered ? by_length(a.p, place.b) : static_cast<int32_t>(place.b);
   const SeqSpan s = seq_span(a.p, b);
   const int64_t all = int64_t(s.n) * group;
-  if (r0 >= all) return;
+  if (r0 >= all || (cut.mixed && all > 16)) return;
   const int32_t rows = all - r0 < 16 ? static_cast<int32_t>(all - r0) : 16;
   const Range tile = tile_range(a, s, r0, rows, cut.by_group);
   const Range part = chunk_of(tile, cut, chunk);
@@ -510,7 +512,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) k_attend_few(AttendArgs a, Cut
       v = Range{v.lo > part.lo ? v.lo : part.lo, v.hi < part.hi ? v.hi : part.hi};
       float rm, rl, y[D / 64];
       careful_row<F, D>(a, b, head, t, h, v, rm, rl, y);
-      careful_store<D>(a, parts, cut.chunks, chunk, t, h, rm, rl, y);
+      careful_store<D>(a, parts, cut.chunks, chunk * parts.rows + (b * heads + head) * 16 + row, t, h, rm, rl, y);
     }
     return;
   }
@@ -536,7 +538,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) k_attend_few(AttendArgs a, Cut
           u32x2{pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv)};
       if (a.lse && d == 0) a.lse[t * a.q_heads + h] = lt != 0.0f ? (base + log2_fast(lt)) * kLn2 : -INFINITY;
     } else {
-      const int64_t at = (int64_t(chunk) * a.p.tokens + t) * a.q_heads + h;
+      const int64_t at = chunk * parts.rows + (b * heads + head) * 16 + row;
       *reinterpret_cast<f32x4*>(parts.o + at * D + d) = y;
       if (d == 0) parts.ml[at] = make_float2(base, lt);
     }
@@ -595,7 +597,7 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attend_many(AttendArgs a, Cut cu
   const int64_t b = place.b;
   const SeqSpan s = seq_span(a.p, b);
   const int64_t all = int64_t(s.n) * group;
-  if (r0 >= all) return;
+  if (r0 >= all || (cut.mixed && all <= 16)) return;
   const int32_t rows = all - r0 < WG ? static_cast<int32_t>(all - r0) : WG;
   const Range tile = tile_range(a, s, r0, rows, cut.by_group);
   const Range part = chunk_of(tile, cut, chunk);
@@ -884,14 +886,14 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attend_many(AttendArgs a, Cut cu
       v = Range{v.lo > part.lo ? v.lo : part.lo, v.hi < part.hi ? v.hi : part.hi};
       float rm, rl, y[D / 64];
       careful_row<F, D>(a, b, head, ti, hi, v, rm, rl, y);
-      careful_store<D>(a, parts, cut.chunks, chunk, ti, hi, rm, rl, y);
+      careful_store<D>(a, parts, cut.chunks, chunk * parts.rows + ti * a.q_heads + hi, ti, hi, rm, rl, y);
     }
     return;
   }
   l += __shfl_xor(l, 32);
   if (c >= wr) return;
   const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-  const int64_t at = (int64_t(chunk) * a.p.tokens + tok) * a.q_heads + qh;
+  const int64_t at = chunk * parts.rows + tok * a.q_heads + qh;
 #pragma unroll
   for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -918,39 +920,53 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attend_many(AttendArgs a, Cut cu
 // two, at most the 256 / (D / 4) chunks that a workgroup reads at once) groups of them a row, and a
 // workgroup as many rows as that leaves room for: the kernel is a chain of loads, and its length is
 // what it costs (32 chunks of 128 rows: 5 us; one wave a row took 10 to 29).
-template <int D>
-__global__ void __launch_bounds__(256)
-    k_attend_join(AttendArgs a, Cut cut, int32_t tile_rows, int32_t lanes, int32_t rows_total, Parts parts) {
+template <int D, bool FEW>
+__global__ void __launch_bounds__(256) k_attend_join(AttendArgs a, Cut cut, int32_t tile_rows, int32_t lanes, Parts parts) {
   constexpr int T = D / 4, G = 256 / T;  // threads of a chunk, chunks at once
   __shared__ __align__(16) f32x4 sh_y[G][T];
   __shared__ float2 sh_ml[G];
   const int x = threadIdx.x % T, y = threadIdx.x / T, part = y & (lanes - 1);
   const int32_t group = static_cast<int32_t>(cut.by_group.d);
-  const uint32_t r = blockIdx.x * (G / lanes) + y / lanes;  // (sequence, token, query head)
-  const uint32_t rt = cut.by_heads.div(r);                  // by_heads: of the queries here
-  const int32_t h = r - rt * cut.by_heads.d;
-  const int64_t b = cut.by_tiles.div(rt);                   // by_tiles: max_new here
-  const int32_t i = rt - static_cast<uint32_t>(b) * cut.by_tiles.d;
-  bool on = r < static_cast<uint32_t>(rows_total);
+  const uint32_t r = blockIdx.x * (G / lanes) + y / lanes;  // row of the parts
+  bool on = r < parts.rows;
   float m = kNoKey, l = 0.0f;
   f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-  int64_t tok = 0;
+  int64_t tok = 0, h = 0;
   if (on) {
+    int64_t b, i;
+    if (FEW) {  // (sequence, head, row)
+      const uint32_t bh = r >> 4, row = r & 15;
+      b = cut.by_heads.div(bh);
+      i = cut.by_group.div(row);
+      h = (bh - static_cast<uint32_t>(b) * cut.by_heads.d) * group + (row - i * group);
+    } else {    // (token, query head): its sequence is the last that starts at or before it
+      tok = cut.by_chunks.div(r);  // by_chunks: the query heads here
+      h = r - static_cast<uint32_t>(tok) * cut.by_chunks.d;
+      int64_t lo = 0, hi = a.p.seqs;
+      while (hi - lo > 1) {
+        const int64_t mid = (lo + hi) >> 1;
+        if (a.p.seq_start[mid] <= tok) lo = mid;
+        else hi = mid;
+      }
+      b = lo;
+      i = 0;
+    }
     const SeqSpan s = seq_span(a.p, b);
-    on = i < s.n;
+    if (!FEW) i = tok - s.tok0;
+    const int64_t all = int64_t(s.n) * group;
+    on = i >= 0 && i < s.n && (!cut.mixed || (all <= 16) == FEW);
     if (on) {
       tok = s.tok0 + i;
-      const int32_t hg = h - static_cast<int32_t>(cut.by_group.div(h)) * group;
-      const int32_t r0 = (i * group + hg) & ~(tile_rows - 1);
-      const int64_t left = int64_t(s.n) * group - r0;
+      const int32_t hg = static_cast<int32_t>(h) - static_cast<int32_t>(cut.by_group.div(static_cast<uint32_t>(h))) * group;
+      const int32_t r0 = (static_cast<int32_t>(i) * group + hg) & ~(tile_rows - 1);
+      const int64_t left = all - r0;
       const Range tile = tile_range(a, s, r0, left < tile_rows ? static_cast<int32_t>(left) : tile_rows, cut.by_group);
       int32_t n = (int64_t(tile.hi) - tile.lo + cut.len - 1) / cut.len;
       n = n < 1 ? 1 : n > cut.chunks ? cut.chunks : n;
-      const int64_t row = tok * a.q_heads + h, step = a.p.tokens * a.q_heads;
 #pragma unroll 4
       for (int32_t k = part; k < n; k += lanes) {
-        const float2 ml = parts.ml[k * step + row];
-        const f32x4 v = *reinterpret_cast<const f32x4*>(parts.o + (k * step + row) * D + 4 * x);
+        const float2 ml = parts.ml[k * parts.rows + r];
+        const f32x4 v = *reinterpret_cast<const f32x4*>(parts.o + (k * parts.rows + r) * D + 4 * x);
         const float mn = fmaxf(m, ml.x), fa = exp2_fast(m - mn), fb = exp2_fast(ml.x - mn);
         l = l * fa + ml.y * fb;
         o = o * fa + v * fb;
@@ -979,83 +995,120 @@ __global__ void __launch_bounds__(256)
 
 }  // namespace
 
-hipError_t launch_paged_attention(const AttendArgs& a, hipStream_t st) {
-  const int64_t group = a.q_heads / a.p.heads;
-  const int64_t rows = a.p.max_new * group;
-  const bool few = rows <= 16;
-  const bool wide = !few && a.p.dim == 128 && a.p.seqs * (rows / 256) * a.p.heads >= 2 * device_cus();
-  const int64_t tile_rows = few ? 16 : wide ? 256 : 128;
-  const int64_t tiles = ceil_div(rows, tile_rows);
-  const int64_t jobs = a.p.seqs * tiles * a.p.heads;  // workgroups without a cut
-  // Cut the keys when the jobs alone do not fill the card.  Prompts: when they leave half of the
-  // workgroups that the CUs hold free.  Decode (1 a CU): a long stream per workgroup costs
-  // least (two sequences of 131072 tokens, 8 heads: 92 us in 256 chunks, 101 in 2048, and the parts'
-  // addition 5 and 7 us), so 1 a CU, and 2 from 8 sequences on, whose ragged lengths then even out; chunks of at
-  // least 1024 keys, below which the second launch costs more than the cut saves (1001 keys: 10.6 us
-  // uncut, 8.6 + 3.9 in halves).  Prompts' steps of 64 keys take 2 us each, so theirs may be shorter:
-  // 512 keys, 256 where they leave most CUs idle.  A window bounds what a causal tile can see.
+namespace {
+
+// One kernel's share of a call: its tiles, how their keys are cut, its parts.
+struct Plan {
+  int64_t tile_rows, jobs;  // jobs: workgroups without a cut
   Cut cut;
-  cut.chunks = 1;
-  cut.len = 0;
-  int64_t span = a.max_kv;
+  Parts parts;
+};
+
+// Cut the keys when the jobs alone do not fill the card.  Prompts: when they leave half of the
+// workgroups that the CUs hold free.  Decode (1 a CU): a long stream per workgroup costs
+// least (two sequences of 131072 tokens, 8 heads: 92 us in 256 chunks, 101 in 2048, and the parts'
+// addition 5 and 7 us), so 1 a CU, and 2 from 8 sequences on, whose ragged lengths then even out; chunks of at
+// least 1024 keys, below which the second launch costs more than the cut saves (1001 keys: 10.6 us
+// uncut, 8.6 + 3.9 in halves).  Prompts' steps of 64 keys take 2 us each, so theirs may be shorter:
+// 512 keys, 256 where they leave most CUs idle.  A window bounds what a causal tile can see.
+Plan plan_for(const AttendArgs& a, bool few, bool mixed, int64_t tile_rows, int64_t tiles) {
+  const int64_t group = a.q_heads / a.p.heads, cus = device_cus();
+  Plan p;
+  p.tile_rows = tile_rows;
+  p.jobs = a.p.seqs * tiles * a.p.heads;
+  int64_t span = a.max_kv, len = 0;
   if (a.causal && a.window > 0) span = std::min(span, a.window + tile_rows / group + 64);
-  const int64_t cus = device_cus();
   if (few) {
-    const int64_t want = ceil_div((a.p.seqs < 8 ? 1 : 2) * cus, jobs);
-    if (want > 1) cut.len = static_cast<int32_t>(std::max<int64_t>(1024, ceil_div(ceil_div(span, want), 64) * 64));
+    const int64_t want = ceil_div((a.p.seqs < 8 ? 1 : 2) * cus, p.jobs);
+    if (want > 1) len = std::max<int64_t>(1024, ceil_div(ceil_div(span, want), 64) * 64);
   } else {
     // tiles that the tokens can fill, and workgroups that fit at once (registers)
-    const int64_t busy = std::min(jobs, (a.p.tokens * group / tile_rows + a.p.seqs) * a.p.heads);
+    const int64_t busy = std::min(p.jobs, (a.p.tokens * group / tile_rows + a.p.seqs) * a.p.heads);
     const int64_t fit = (a.p.dim == 64 ? 3 : 2) * cus;
     if (2 * busy <= fit)
-      cut.len = static_cast<int32_t>(
-          std::max<int64_t>(4 * busy > cus ? 512 : 256, ceil_div(ceil_div(span, ceil_div(fit, busy)), 64) * 64));
+      len = std::max<int64_t>(4 * busy > cus ? 512 : 256, ceil_div(ceil_div(span, ceil_div(fit, busy)), 64) * 64);
   }
-  if (cut.len > 0) cut.chunks = static_cast<int32_t>(ceil_div(span, cut.len));
-  if (cut.chunks == 1) cut.len = 64;
-  cut.ordered = few && cut.chunks == 1 && jobs > device_cus() && a.p.seqs <= 64;
-  Parts parts{nullptr, nullptr};
-  if (cut.chunks > 1) {
-    const size_t n = size_t(cut.chunks) * a.p.tokens * a.q_heads;
-    void* p = nullptr;
-    const hipError_t e = get_scratch(st, n * (a.p.dim + 2) * sizeof(float), &p);
-    if (e != hipSuccess) return e;
-    parts.o = static_cast<float*>(p);
-    parts.ml = reinterpret_cast<float2*>(parts.o + n * a.p.dim);
-  }
-  const int64_t grid = jobs * cut.chunks;
-  cut.by_heads = FastDiv(a.p.heads);
-  cut.by_tiles = FastDiv(static_cast<uint32_t>(tiles));
-  cut.by_chunks = FastDiv(cut.chunks);
-  cut.by_group = FastDiv(static_cast<uint32_t>(group));
-  const int waves = few || wide ? 8 : 4;
-  auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(grid), dim3(64 * waves), 0, st, a, cut, parts); };
-  auto by_dim = [&](auto f) {
-    constexpr int F = decltype(f)::value;
-    if (few)
-      a.p.dim == 128 ? go(k_attend_few<F, 128>) : go(k_attend_few<F, 64>);
-    else
-      wide ? go(k_attend_many<F, 128, 8>) : a.p.dim == 128 ? go(k_attend_many<F, 128, 4>) : go(k_attend_many<F, 64, 4>);
+  Cut& c = p.cut;
+  c.chunks = len > 0 ? static_cast<int32_t>(ceil_div(span, len)) : 1;
+  c.len = c.chunks > 1 ? static_cast<int32_t>(len) : 64;
+  c.ordered = few && c.chunks == 1 && p.jobs > cus && a.p.seqs <= 64;
+  c.mixed = mixed;
+  c.by_heads = FastDiv(a.p.heads);
+  c.by_tiles = FastDiv(static_cast<uint32_t>(tiles));
+  c.by_chunks = FastDiv(c.chunks);
+  c.by_group = FastDiv(static_cast<uint32_t>(group));
+  p.parts = Parts{nullptr, nullptr, few ? a.p.seqs * a.p.heads * 16 : a.p.tokens * a.q_heads};
+  return p;
+}
+
+size_t part_floats(const Plan& p, int dim) {
+  return p.cut.chunks > 1 ? size_t(p.cut.chunks) * p.parts.rows * (dim + 2) : 0;
+}
+
+template <typename K>
+hipError_t launch_tiles(K kern, const AttendArgs& a, const Plan& p, int waves, hipStream_t st) {
+  hipLaunchKernelGGL(kern, dim3(p.jobs * p.cut.chunks), dim3(64 * waves), 0, st, a, p.cut, p.parts);
+  return hipGetLastError();
+}
+
+template <bool FEW>
+hipError_t launch_join(const AttendArgs& a, const Plan& p, hipStream_t st) {
+  Cut cut = p.cut;
+  if (!FEW) cut.by_chunks = FastDiv(static_cast<uint32_t>(a.q_heads));
+  const int32_t at_once = 1024 / a.p.dim;
+  int32_t lanes = 1;
+  while (lanes < at_once && lanes < cut.chunks) lanes <<= 1;
+  const dim3 grid(static_cast<uint32_t>(ceil_div(p.parts.rows, at_once / lanes)));
+  auto go = [&](auto kern) {
+    hipLaunchKernelGGL(kern, grid, dim3(256), 0, st, a, cut, static_cast<int32_t>(p.tile_rows), lanes, p.parts);
   };
-  if (a.p.fmt == FP8RT_E4M3)
-    by_dim(std::integral_constant<int, kE4M3>{});
-  else
-    by_dim(std::integral_constant<int, kE5M2>{});
-  hipError_t e = hipGetLastError();
-  if (e == hipSuccess && cut.chunks > 1) {
-    cut.by_heads = FastDiv(static_cast<uint32_t>(a.q_heads));
-    cut.by_tiles = FastDiv(static_cast<uint32_t>(a.p.max_new));
-    const int32_t all = static_cast<int32_t>(a.p.seqs * a.p.max_new * a.q_heads), at_once = 1024 / a.p.dim;
-    int32_t lanes = 1;
-    while (lanes < at_once && lanes < cut.chunks) lanes <<= 1;
-    const dim3 jg(static_cast<uint32_t>(ceil_div(all, at_once / lanes)));
-    auto join = [&](auto kern) {
-      hipLaunchKernelGGL(kern, jg, dim3(256), 0, st, a, cut, static_cast<int32_t>(tile_rows), lanes, all, parts);
+  a.p.dim == 128 ? go(k_attend_join<128, FEW>) : go(k_attend_join<64, FEW>);
+  return hipGetLastError();
+}
+
+template <int F>
+hipError_t launch_attention(const AttendArgs& a, hipStream_t st) {
+  const int64_t rows = a.p.max_new * (a.q_heads / a.p.heads);
+  // A batch whose sequences bring at most half of max_new on average may hold single tokens beside
+  // prompts; a prompt's workgroup would read such a sequence at one wave's pace, so each kernel
+  // then runs for its own (one prompt of 2000 tokens among 64 / 200 sequences of 4000, 64 / 8 heads: 229 / 501 us,
+  // in one kernel 393 / 907; where no sequence is short the second launch costs 3.5).
+  const bool few = rows <= 16;
+  const bool mixed = !few && a.q_heads / a.p.heads <= 16 && 2 * a.p.tokens <= a.p.seqs * a.p.max_new;
+  const bool wide = !few && a.p.dim == 128 && a.p.seqs * (rows / 256) * a.p.heads >= 2 * device_cus();
+  const int64_t tile_rows = wide ? 256 : 128;
+  Plan f = plan_for(a, true, mixed, 16, 1), m = plan_for(a, false, mixed, tile_rows, ceil_div(rows, tile_rows));
+  const size_t nf = few || mixed ? part_floats(f, a.p.dim) : 0, nm = few ? 0 : part_floats(m, a.p.dim);
+  if (nf + nm > 0) {
+    void* mem = nullptr;
+    const hipError_t e = get_scratch(st, (nf + nm) * sizeof(float), &mem);
+    if (e != hipSuccess) return e;
+    auto place = [&](Plan& p, float* at) {
+      p.parts.o = at;
+      p.parts.ml = reinterpret_cast<float2*>(at + size_t(p.cut.chunks) * p.parts.rows * a.p.dim);
     };
-    a.p.dim == 128 ? join(k_attend_join<128>) : join(k_attend_join<64>);
-    e = hipGetLastError();
+    place(f, static_cast<float*>(mem));
+    place(m, static_cast<float*>(mem) + nf);
+  }
+  hipError_t e = hipSuccess;
+  if (few || mixed) {
+    e = a.p.dim == 128 ? launch_tiles(k_attend_few<F, 128>, a, f, kFewWaves, st)
+                       : launch_tiles(k_attend_few<F, 64>, a, f, kFewWaves, st);
+    if (e == hipSuccess && f.cut.chunks > 1) e = launch_join<true>(a, f, st);
+  }
+  if (!few && e == hipSuccess) {
+    e = wide              ? launch_tiles(k_attend_many<F, 128, 8>, a, m, 8, st)
+        : a.p.dim == 128 ? launch_tiles(k_attend_many<F, 128, 4>, a, m, 4, st)
+                         : launch_tiles(k_attend_many<F, 64, 4>, a, m, 4, st);
+    if (e == hipSuccess && m.cut.chunks > 1) e = launch_join<false>(a, m, st);
   }
   return e;
+}
+
+}  // namespace
+
+hipError_t launch_paged_attention(const AttendArgs& a, hipStream_t st) {
+  return a.p.fmt == FP8RT_E4M3 ? launch_attention<kE4M3>(a, st) : launch_attention<kE5M2>(a, st);
 }
 
 }  // namespace fp8rt

@@ -137,6 +137,15 @@ def test_many_sequences(rt, seqs):
     run(rt, ref.Batch([2] * seqs, before, 32), 8, 1, 128, window=50)
 
 
+@pytest.mark.parametrize("dim,heads,group", [(128, 2, 4), (64, 1, 5), (128, 2, 17)])
+def test_prompts_among_single_tokens(rt, dim, heads, group):
+    """Sequences with one, few, many and no new tokens in one call, short and long contexts: both kernels run,
+    with and without their keys cut."""
+    run(rt, ref.Batch([1, 70, 0, 3, 1, 4, 200, 1, 5], [900, 0, 7, 40, 2600, 5, 30, 0, 1300], 16), heads, group, dim)
+    run(rt, ref.Batch([1, 40, 2], [5000, 10, 1], 32), heads, group, dim, window=2000)
+    run(rt, ref.Batch([1, 40] + [1] * 30, [50, 300] + [17 * i for i in range(30)], 64), heads, group, dim, causal=False)
+
+
 def test_long_context(rt):
     run(rt, ref.Batch([1, 1, 2], [9000, 20, 4000], 64), 2, 8, 128)
     run(rt, ref.Batch([1], [9000], 16), 1, 4, 64, window=5000)
