@@ -3,17 +3,18 @@
 //
 // Mathematics.  With t_j = z_j log2(e) the scores of the visible positions and
 // v_j = s_j dec(code_j) their values (s_j the page's v scale), the weight
-//   w_j = 2^(t_j + log2 s_j - m),   m at most 15 below the maximum of t_j + log2 s_j,
+//   w_j = 2^(t_j + log2 s_j - m + 8),   m at most 8 below the maximum of t_j + log2 s_j,
 // turns the output into  y = sum_j w_j dec(code_j) / sum_j (w_j / s_j):  the codes go
 // into the second matrix product as they are, the weights stay within
 // fp16 whatever the pages' scales, and the sums follow in one pass over the keys
 // (when m moves, the sums so far are multiplied by 2^(m_old - m_new)).
-// m + log2 sum_j (w_j / s_j) is the log-sum-exp in base 2.
+// The denominator is kept as l = sum_j 2^(t_j - m), so m + log2 l is the log-sum-exp in base 2.
 //
 // Roundings.  Every FP8 code is a bf16 and an fp16 value, so q k multiplies exact
 // operands (bf16 MFMA) and the codes enter the second product exactly (fp16 MFMA); the weights are
 // rounded to fp16 (11 bits; bf16's 8 bits would add as much error as the bf16
-// output itself has); sums, maxima and accumulators are binary32.
+// output itself has): from 2^-22 of the row's largest on they keep those bits, below they are rounded to
+// multiples of 2^-32 of it.  Sums, maxima and accumulators are binary32.
 //
 // Orientation.  The scores are computed transposed, S^T = K Q^T: a lane then holds
 // one query row's scores for several keys, which is the operand layout that the
@@ -45,8 +46,13 @@ typedef short i16x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // The reference m follows the running maximum only when weights grow too large for
-// fp16: when a lane's weights of one 16-key part add up to this.
-constexpr float kFull = 32768.0f;
+// fp16: when a lane's weights of one 16-key part add up to its largest value.
+constexpr float kFull = 65504.0f;
+// When m has followed, the largest weight is 2^kLift: fp16 ends 2^-24 below 1, and where one key outweighs the rest (an
+// attention sink, or a key in a page of large values) the small weights make the output.  The room left above sets how
+// often m follows: a prompt of 8192 tokens takes 1096 us without a lift, 1105 with 6, 1108 with 8, 1124 with 10.
+// Without a lift, 8192 keys 18 nats below one whose value is 0 come out as 0 (prompts) or 13% off (decode).
+constexpr float kLift = 8.0f, kUnlift = 0x1p-8f;
 // Before a row has seen a key, m is this: any score then gives an infinite
 // weight, which makes m follow.
 constexpr float kNoKey = -1e30f;
@@ -191,7 +197,8 @@ struct Parts {
   int64_t rows;
 };
 
-// What one 16-key part of a step needs from its page: t = dot * c, log2 of the v scale, its inverse.
+// What one 16-key part of a step needs from its page: t = dot * c, log2 of the v scale with the lift, the factor that
+// turns a weight into 2^(t - m).
 // A page that is not there gives weights of 0 (its codes are staged as 0).  Scales that are not
 // finite count as 1 here; the rows are done again by careful_row.
 struct PartScale {
@@ -201,8 +208,8 @@ __device__ __forceinline__ bool finite_scales(float ks, float vs) { return ks <=
 __device__ __forceinline__ PartScale part_scale(bool there, float ks, float vs, float sm) {
   const bool fine = finite_scales(ks, vs);
   const float c = fine ? ks * sm : 1.0f, v = fine && vs >= kTinyScale ? vs : fine ? kTinyScale : 1.0f;
-  return PartScale{c < kTinyScale ? kTinyScale : c, there ? log2_fast(v) : -INFINITY,
-                   there ? __builtin_amdgcn_rcpf(v) : 0.0f};  // (rcp: 1 ulp)
+  return PartScale{c < kTinyScale ? kTinyScale : c, there ? log2_fast(v) + kLift : -INFINITY,
+                   there ? __builtin_amdgcn_rcpf(v) * kUnlift : 0.0f};  // (rcp: 1 ulp)
 }
 
 // One query row over the keys [see.lo, see.hi), by one wave, without products that hidden keys take
@@ -454,7 +461,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) k_attend_few(AttendArgs a, Cut
         top = fmaxf(top, fmaf(fmaxf(fmaxf(z[t][0], z[t][1]), fmaxf(z[t][2], z[t][3])), ps[t].c, ps[t].lv));
       top = fmaxf(top, __shfl_xor(top, 16));
       top = fmaxf(top, __shfl_xor(top, 32));
-      const float mn = fmaxf(m, top);
+      const float mn = fmaxf(m, top - kLift);
       const float fade = exp2_fast(m - mn);
       l *= fade;
 #pragma unroll
@@ -533,13 +540,13 @@ __global__ void __launch_bounds__(64 * kFewWaves) k_attend_few(AttendArgs a, Cut
     const int32_t rr = r0 + row, ri = cut.by_group.div(rr);
     const int64_t t = s.tok0 + ri, h = int64_t(head) * group + (rr - ri * group);
     if (cut.chunks == 1) {
-      const float inv = lt != 0.0f ? 1.0f / lt : 0.0f;
+      const float inv = lt != 0.0f ? kUnlift / lt : 0.0f;
       *reinterpret_cast<u32x2*>(a.y + t * a.ldy + h * a.hdy + d) =
           u32x2{pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv)};
       if (a.lse && d == 0) a.lse[t * a.q_heads + h] = lt != 0.0f ? (base + log2_fast(lt)) * kLn2 : -INFINITY;
     } else {
       const int64_t at = chunk * parts.rows + (b * heads + head) * 16 + row;
-      *reinterpret_cast<f32x4*>(parts.o + at * D + d) = y;
+      *reinterpret_cast<f32x4*>(parts.o + at * D + d) = y * kUnlift;
       if (d == 0) parts.ml[at] = make_float2(base, lt);
     }
   }
@@ -785,7 +792,7 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attend_many(AttendArgs a, Cut cu
             top = fmaxf(top, fmaf(x, pc[e], plv[e]));
           }
           top = fmaxf(top, __shfl_xor(top, 32));
-          const float mn = fmaxf(m, top);
+          const float mn = fmaxf(m, top - kLift);
           const float fade = exp2_fast(m - mn);
           l *= fade;
 #pragma unroll
@@ -892,7 +899,7 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attend_many(AttendArgs a, Cut cu
   }
   l += __shfl_xor(l, 32);
   if (c >= wr) return;
-  const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+  const float inv = l != 0.0f ? kUnlift / l : 0.0f;
   const int64_t at = chunk * parts.rows + tok * a.q_heads + qh;
 #pragma unroll
   for (int d = 0; d < DT; ++d)
@@ -904,7 +911,7 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attend_many(AttendArgs a, Cut cu
         *reinterpret_cast<u32x2*>(a.y + tok * a.ldy + qh * a.hdy + dim) =
             u32x2{pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv)};
       else
-        *reinterpret_cast<f32x4*>(parts.o + at * D + dim) = y;
+        *reinterpret_cast<f32x4*>(parts.o + at * D + dim) = y * kUnlift;
     }
   if (h == 0) {
     if (cut.chunks > 1)

@@ -542,9 +542,9 @@ fp8rt_status fp8_kv_append(const void* k, const void* v, fp8rt_dtype xt, int64_t
  * window > 0; j's page present.  Hidden positions count for nothing whatever they hold (NaN
  * codes or scales, stale or missing pages).  A query that sees no position gives y = 0 and lse = -Inf.
  * Keys and queries are multiplied as bf16 (every FP8 value is one) and
- * accumulated in FP32; softmax statistics are FP32; the weights e^(z - m) are
- * rounded to fp16 (11 bits, times the page's v scale relative to the largest seen) for the
- * second product, whose accumulation is FP32.
+ * accumulated in FP32; softmax statistics are FP32; the weights e^(z - m), times their page's v scale,
+ * are rounded to fp16 for the second product, whose accumulation is FP32: 11 bits for a weight of at
+ * least 2^-22 of its row's largest, below that an absolute error of at most 2^-33 of the largest.
  *   q : bf16, token t, head h, element d at [t * ldq + h * hdq + d] (qt must be FP8RT_BF16)
  *   y : bf16, at [t * ldy + h * hdy + d] (yt must be FP8RT_BF16);
  *   lse : nullable fp32 [tokens][q_heads]: m + ln(sum_j e^(z[j] - m))
