@@ -721,7 +721,7 @@ fp8rt_status fp8_paged_attention(const void* q, fp8rt_dtype qt, int64_t tokens, 
   a.max_kv = std::min(max_kv, table_pages * page_size);
   a.sm_scale = sm_scale;
   a.causal = causal != 0;
-  a.window = window;
+  a.window = std::min(window, int64_t(1) << 31);  // positions lie below 2^31: a wider one hides nothing
   a.y = static_cast<uint16_t*>(y);
   a.ldy = ldy;
   a.hdy = hdy;

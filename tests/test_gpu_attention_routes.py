@@ -1,5 +1,5 @@
 """fp8_paged_attention on the routes that few calls take: the widest workgroups with their keys cut, alone and
-beside single tokens; bounds looser than the batch."""
+beside single tokens; bounds looser than the batch; windows of any size."""
 import pytest
 import torch
 
@@ -37,3 +37,22 @@ def test_bounds_looser_than_the_batch(rt):
         bt.max_new, bt.max_kv = max_new, max_kv
         run(rt, bt, 2, 4, 64)
         run(rt, bt, 2, 4, 128, causal=False, window=37)
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31, 2 ** 62, 2 ** 63 - 1])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("new", [1, 40])
+def test_a_window_wider_than_any_sequence_hides_nothing(rt, window, causal, new):
+    """kv_len below the number of new tokens among them: those queries stand before position 0."""
+    bt = ref.Batch([new, 3, 4], [2000, -2, 0], 16)
+    kc, vc, ks, vs = (t.cuda() for t in make(bt, 2, 64, 0, 12))
+    q = torch.randn(bt.tokens, 8, 64, generator=torch.Generator().manual_seed(4)).bfloat16().cuda()
+    plan = [t.cuda() for t in (bt.table, bt.start, bt.kv_len)]
+
+    def call(window):
+        y, lse = torch.full_like(q, 7.0), torch.full((bt.tokens, 8), 7.0).cuda()
+        rt.fp8_paged_attention(q, kc, vc, ks, vs, 0, *plan, bt.max_new, bt.max_kv, 0.125, y, causal=causal,
+                               window=window, lse=lse)
+        return y, lse
+
+    assert all(torch.equal(a, b) for a, b in zip(call(window), call(0)))
