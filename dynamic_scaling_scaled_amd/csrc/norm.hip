@@ -268,6 +268,8 @@ __global__ void __launch_bounds__(1024) k_rmsnorm_backward(NormGradArgs a, RowSh
     for (int v = 0; v < NV; ++v) {
       const int o = v * per + tr;
       load_weight(a.w, a.wt, (o < octets ? o : 0) * 8, w[v]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[v][i] = o < octets ? w[v][i] : 0.0f;  // (0 * a weight that is not finite)
     }
   };
   if (kHold) weights();

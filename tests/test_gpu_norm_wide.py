@@ -1,4 +1,7 @@
-"""Rows wider than one octet a thread, more of them than workgroups (so that every workgroup loops over rows): the norm's and its gradient's bounds are those of test_gpu_norm."""
+"""Rows wider than one octet a thread, more of them than workgroups (so that every workgroup loops over rows),
+and weights that are not finite: the norm's and its gradient's bounds are those of test_gpu_norm."""
+import math
+
 import pytest
 import torch
 
@@ -42,3 +45,19 @@ def test_norm_of_wide_rows(rt, rows, cols, dtype):
     check_norm(rt, rows, cols, dtype=dtype, pad=16)
     check_norm(rt, rows, cols, dtype=dtype, gran=(1, 128), alias="res")
     check_norm(rt, rows, cols, dtype=dtype, gran=(0, 0), mode=rt.GIVEN, residual=False)
+
+
+@pytest.mark.parametrize("cols", [16, 48, 512, 1024, 1040, 8208, 16400])
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
+def test_gradient_with_a_weight_that_is_not_finite(rt, cols, value):
+    """The formula's infinities and NaN, whether or not a row fills its threads."""
+    rows = 3
+    dy, h, w, rstd, _ = grad_inputs(rows, cols, torch.float32, torch.float32, 0, False)
+    w[0] = value
+    dx, dw = torch.empty_like(dy), torch.empty(cols).cuda()
+    rt.fp8_rmsnorm_backward(dy, h, w, rstd, dx, dw)
+    want, wdw, _, wterms = ref.norm_grad(dy.cpu(), h.cpu(), w.cpu(), rstd.cpu(), None)
+    got = dx.cpu().double()
+    assert torch.equal(got.isnan(), want.isnan())
+    assert torch.equal(got.nan_to_num(0, 1, -1), want.nan_to_num(0, 1, -1))  # (nothing in such a row is finite)
+    assert bool(((dw.cpu().double() - wdw).abs() <= 76 * U * wterms).all())  # the weight has no part in it
