@@ -3,7 +3,7 @@
 //
 // Mathematics.  With t_j = z_j log2(e) the scores of the visible positions and
 // v_j = s_j dec(code_j) their values (s_j the page's v scale), the weight
-//   w_j = 2^(t_j + log2 s_j - m + 8),   m at most 8 below the maximum of t_j + log2 s_j,
+//   w_j = 2^(t_j + log2 s_j - m + 8),   m at most 8 below the maximum of t_j + max(log2 s_j, -90),
 // turns the output into  y = sum_j w_j dec(code_j) / sum_j (w_j / s_j):  the codes go
 // into the second matrix product as they are, the weights stay within
 // fp16 whatever the pages' scales, and the sums follow in one pass over the keys
@@ -53,6 +53,9 @@ constexpr float kFull = 65504.0f;
 // often m follows: a prompt of 8192 tokens takes 1096 us without a lift, 1105 with 6, 1108 with 8, 1124 with 10.
 // Without a lift, 8192 keys 18 nats below one whose value is 0 come out as 0 (prompts) or 13% off (decode).
 constexpr float kLift = 8.0f, kUnlift = 0x1p-8f;
+// m stays within this of the scores however small the v scales are (2^-112 is the smallest that append writes): a term
+// 2^(t - m) of the denominator is then at most 2^90, which leaves room for its sum, and the largest weight at least 2^-14.
+constexpr float kReach = 90.0f;
 // Before a row has seen a key, m is this: any score then gives an infinite
 // weight, which makes m follow.
 constexpr float kNoKey = -1e30f;
@@ -211,6 +214,9 @@ __device__ __forceinline__ PartScale part_scale(bool there, float ks, float vs, 
   return PartScale{c < kTinyScale ? kTinyScale : c, there ? log2_fast(v) + kLift : -INFINITY,
                    there ? __builtin_amdgcn_rcpf(v) * kUnlift : 0.0f};  // (rcp: 1 ulp)
 }
+
+// log2 of a part's v scale (with the lift) as m follows it.  Absent pages stay at -Inf.
+__device__ __forceinline__ float reached(float lv) { return lv > -INFINITY ? fmaxf(lv, kLift - kReach) : lv; }
 
 // One query row over the keys [see.lo, see.hi), by one wave, without products that hidden keys take
 // part in: m, l = sum 2^(t - m) and this lane's D/64 dimensions of sum 2^(t - m) v.  The matrix
@@ -458,7 +464,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) k_attend_few(AttendArgs a, Cut
       float top = kNoKey;
 #pragma unroll
       for (int t = 0; t < 2; ++t)
-        top = fmaxf(top, fmaf(fmaxf(fmaxf(z[t][0], z[t][1]), fmaxf(z[t][2], z[t][3])), ps[t].c, ps[t].lv));
+        top = fmaxf(top, fmaf(fmaxf(fmaxf(z[t][0], z[t][1]), fmaxf(z[t][2], z[t][3])), ps[t].c, reached(ps[t].lv)));
       top = fmaxf(top, __shfl_xor(top, 16));
       top = fmaxf(top, __shfl_xor(top, 32));
       const float mn = fmaxf(m, top - kLift);
@@ -789,7 +795,7 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attend_many(AttendArgs a, Cut cu
             float x = -INFINITY;
 #pragma unroll
             for (int i = 0; i < 8; ++i) x = fmaxf(x, z[kt][8 * (e % 2) + i]);
-            top = fmaxf(top, fmaf(x, pc[e], plv[e]));
+            top = fmaxf(top, fmaf(x, pc[e], reached(plv[e])));
           }
           top = fmaxf(top, __shfl_xor(top, 32));
           const float mn = fmaxf(m, top - kLift);
