@@ -251,7 +251,7 @@ struct NormGradArgs {
   int64_t lddx = 0;
   float* dw = nullptr;
 };
-constexpr int64_t kNormMaxCols = 32768;  // 1024 threads hold a row, 32 elements each
+constexpr int64_t kNormMaxCols = 32768;  // 1024 threads take a row, 32 elements each (partly spilled above 16384)
 hipError_t launch_rmsnorm_backward(const NormGradArgs& a, hipStream_t stream);
 
 // The paged FP8 cache of keys and values (kv_append.hip, paged_attention.hip).

@@ -5,7 +5,7 @@
 // what it receives, the scale (that of the page's earlier tokens if it is
 // larger), the earlier tokens' codes again if the scale grew, the new codes.
 // Bound by HBM for prompts (2 or 4 bytes read, 1 written per element; five ragged prompts of
-// together 11.8 thousand tokens, 8 heads of 128, pages of 16: 16 us, 4.6 TB/s), by launch and two
+// together 11.8 thousand tokens, 8 heads of 128, pages of 16: 16 to 18 us, 4.0 to 4.6 TB/s), by launch and two
 // dependent loads for single tokens (64 sequences: 4.1 us).  A wave needs no barrier, and a page of up to 32 tokens
 // (64 at 64 dimensions) is read once.
 #include "paged_common.h"

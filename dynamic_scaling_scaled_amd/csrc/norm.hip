@@ -9,11 +9,14 @@
 //   dh_j = c (g_j - n_j mean_k(g_k n_k)),  g = dy w, n = h c;   dw_j = sum_rows dy_j n_j.
 //
 // Both are bound by HBM: the forward moves x, residual, h and one byte of code per element,
-// the gradient dy, h, the residual's gradient and dx.  A row stays in registers between its
-// reduction and its use, so every element is read once; workgroups loop over rows with the next
-// row's loads in flight, since one row a workgroup leaves the memory idle during its reduction.
+// the gradient dy, h, the residual's gradient and dx.  Up to 16384 columns a row stays in registers between its
+// reduction and its use (fp32 rows of the forward spill 2 of them); workgroups loop over rows, the forward up to 16384
+// and the gradient up to 8192 columns with the next
+// row's loads in flight, since one row a workgroup leaves the memory idle during its reduction.  Above 16384
+// columns a thread holds 4 octets, of which 32 to 46 registers (forward) and 78 to 93 (gradient) spill.
 // Measured at 4096 x 8192 bf16 with residual: forward 45 us (5.2 TB/s), gradient 48 + 4 us for
-// dweight's shares (5.3 TB/s); a device copy of as many bytes reaches 4.7 to 5.2.  8189 x 7168 in 1x128
+// dweight's shares (5.3 TB/s); a device copy of as many bytes reaches 4.7 to 5.2.  4096 x 16384: 89 us (5.3 TB/s) and
+// 109 (4.9); 4096 x 32768: 241 (3.9) and 499 (2.2).  8189 x 7168 in 1x128
 // groups: 93 us (4.4 TB/s), the groups' scales (two exact quotients per group) taking the rest.  One
 // row of 8192: 4.1 us, launch and one chain of loads and reductions.
 #include <algorithm>
@@ -388,8 +391,8 @@ __global__ void __launch_bounds__(256) k_dweight_sum(const float* part, int n, i
 //  - Few rows (under 2 a CU): one octet a thread, the shortest chain.
 //  - Many rows: nv_many octets a thread, looped over by threads_per_cu threads a CU.  Measured at
 //    4096 x 8192 bf16 with residual, us for 1 / 2 / 4 octets: forward 59 / 49 / 74 with 1024 threads a
-//    CU, 61 / 49 / 80 with 2048; gradient 53 / 101 / 302 (dweight's sums spill from 2 on) with 512,
-//    56 / 107 / 280 with 2048.  One workgroup a row, no loop: 69 and 65.
+//    CU, 61 / 49 / 80 with 2048; gradient 53 / 101 / 302 (2 octets leave no registers for the next row, 4 spill) with
+//    512, 56 / 107 / 280 with 2048.  One workgroup a row, no loop: 69 and 65.
 struct Launch {
   RowShape shape;
   int nv, threads;

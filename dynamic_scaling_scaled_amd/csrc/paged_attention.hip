@@ -179,8 +179,8 @@ __device__ __forceinline__ Range chunk_of(const Range& t, const Cut& c, int32_t 
                i == c.chunks - 1 || hi > t.hi ? t.hi : static_cast<int32_t>(hi)};
 }
 
-// The sequence of rank `slot` by falling length, of at most 64 (one a lane).  Where workgroups
-// outnumber the places on the card, the long ones must not start last.
+// The sequence of rank `slot` by falling length, of at most 64 (one a lane; larger batches run in their
+// own order).  Where workgroups outnumber the places on the card, the long ones must not start last.
 __device__ __forceinline__ int32_t by_length(const PagedArgs& p, int32_t slot) {
   const int32_t lane = threadIdx.x & 63, n = static_cast<int32_t>(p.seqs);
   const int32_t len = p.kv_len[lane < n ? lane : 0];
@@ -567,11 +567,11 @@ __global__ void __launch_bounds__(64 * kFewWaves) k_attend_few(AttendArgs a, Cut
 // touch every bank once.
 // Bound by issue: a tile and wave are 32 matrix instructions (1024 cycles), about 235 vector
 // instructions, 32 exponentials among them (1080 cycles), and LDS reads that a CU's waves
-// share (a wave's 32 rows use each operand once).  Matrix cores busy 45% of the time, vector units 47%.  64 rows
+// share (a wave's 32 rows use each operand once).  Matrix cores busy 44% of the time, vector units 47%.  64 rows
 // a wave would halve the LDS reads, but leave one wave a SIMD and move accumulators between register
 // files: 1666 us against 1288 then.  8 waves share a tile's widening: 1131 us against 1228 with 4.
-// An 8192-token prompt, 64 heads over 8 of 128: 1086 to 1115 us, 1.0 PFLOP/s, where a bf16 library
-// product of 8192^3 reaches 1.19 on the same card.
+// An 8192-token prompt, 64 heads over 8 of 128: 1.08 to 1.15 ms between cards, 0.96 to 1.02 PFLOP/s, where a bf16
+// library product of 8192^3 reaches 1.19.
 constexpr int kBK = 64;
 
 template <int D>
@@ -1024,6 +1024,10 @@ struct Plan {
 // least 1024 keys, below which the second launch costs more than the cut saves (1001 keys: 10.6 us
 // uncut, 8.6 + 3.9 in halves).  Prompts' steps of 64 keys take 2 us each, so theirs may be shorter:
 // 512 keys, 256 where they leave most CUs idle.  A window bounds what a causal tile can see.
+// The host knows bounds only.  Sequences drawn evenly from 1 to 8192 tokens even out (64 / 96 / 128 of them, 8 heads: 107 / 157 /
+// 190 us for 94 / 131 / 164 of reading); a single long one does not, since its workgroups are as many as a short one's (131072 tokens
+// among 63 / 31 sequences of 1000: 724 / 369 us for 65 / 54 of reading).  A max_kv far above the lengths makes one chunk of
+// each sequence and still pays for the join (8 of 2000 tokens: 17 us, under a bound of 131072 24).
 Plan plan_for(const AttendArgs& a, bool few, bool mixed, int64_t tile_rows, int64_t tiles) {
   const int64_t group = a.q_heads / a.p.heads, cus = device_cus();
   Plan p;
@@ -1035,7 +1039,8 @@ Plan plan_for(const AttendArgs& a, bool few, bool mixed, int64_t tile_rows, int6
     const int64_t want = ceil_div((a.p.seqs < 8 ? 1 : 2) * cus, p.jobs);
     if (want > 1) len = std::max<int64_t>(1024, ceil_div(ceil_div(span, want), 64) * 64);
   } else {
-    // tiles that the tokens can fill, and workgroups that fit at once (registers)
+    // tiles that the tokens can fill, and workgroups that fit at once (registers; of the widest only
+    // half as many do, which then run in two rounds)
     const int64_t busy = std::min(p.jobs, (a.p.tokens * group / tile_rows + a.p.seqs) * a.p.heads);
     const int64_t fit = (a.p.dim == 64 ? 3 : 2) * cus;
     if (2 * busy <= fit)
@@ -1085,7 +1090,8 @@ hipError_t launch_attention(const AttendArgs& a, hipStream_t st) {
   // A batch whose sequences bring at most half of max_new on average may hold single tokens beside
   // prompts; a prompt's workgroup would read such a sequence at one wave's pace, so each kernel
   // then runs for its own (one prompt of 2000 tokens among 64 / 200 sequences of 4000, 64 / 8 heads: 229 / 501 us,
-  // in one kernel 393 / 907; where no sequence is short the second launch costs 3.5).
+  // in one kernel 393 / 907; where no sequence is short the second launch costs 3.5).  Fewer single tokens than
+  // prompts do not meet this: one prompt of 2000 tokens and one token behind 32768 take 848 us, in two calls 100 and 20.
   const bool few = rows <= 16;
   const bool mixed = !few && a.q_heads / a.p.heads <= 16 && 2 * a.p.tokens <= a.p.seqs * a.p.max_new;
   const bool wide = !few && a.p.dim == 128 && a.p.seqs * (rows / 256) * a.p.heads >= 2 * device_cus();

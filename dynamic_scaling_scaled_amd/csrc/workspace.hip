@@ -1,7 +1,8 @@
 // workspace.hip -- per-(device, stream) device memory of the library: the
 // per-block partials of the quantize kernels (a fixed 256 KB workspace) and a
 // scratch buffer for the GEMM's repacked block scales, the FP32 parts of a
-// split last wave and the cast-transpose's per-group arrays.
+// split last wave, the cast-transpose's per-group arrays, the shares of a norm's
+// weight gradient and the parts of attention cut along its keys.
 //
 // Lifetime rules, chosen so that a HIP graph captured after warm-up stays
 // valid:

@@ -465,8 +465,8 @@ fp8rt_status fp8_granularity_ledger(const void* w, fp8rt_dtype wt, int64_t N, in
  * inv_scale if not NULL, else r = fl32(1/s)).
  * norm_eps: finite, >= 0.  Alignment as fp8_quantize: cols and leading
  * dimensions multiples of 16, pointers of matrices and weight 16-byte aligned.
- * cols <= 32768 (a row stays in registers), else FP8RT_EUNSUPPORTED.  Workspace: the per-stream workspace holds the amax partials
- * of the {0,0} case. */
+ * cols <= 32768 (32 elements for each of a workgroup's 1024 threads), else FP8RT_EUNSUPPORTED.
+ * Workspace: the per-stream workspace holds the amax partials of the {0,0} case. */
 fp8rt_status fp8_rmsnorm_quantize(const void* x, fp8rt_dtype xt, int64_t rows, int64_t cols, int64_t ldx,
                                   const void* residual, int64_t ldr, const void* weight, fp8rt_dtype wt,
                                   float norm_eps, fp8rt_gran g, fp8rt_format f, fp8rt_mode mode, float eps,
@@ -554,9 +554,11 @@ fp8rt_status fp8_kv_append(const void* k, const void* v, fp8rt_dtype xt, int64_t
  * q_heads a multiple of heads; sm_scale finite; window >= 0; at most 2^22 tiles of
  * 128 (token, head of a group) rows over all sequences and heads (else FP8RT_EUNSUPPORTED).
  * Alignment: ldq, hdq multiples of 8, ldy, hdy of 4, q and the caches 16-byte, y 8-byte aligned.
- * Scratch: the per-stream scratch buffer holds the parts of key ranges cut into chunks
- * (chunks x tokens x q_heads x (head_dim + 2) floats; the number of chunks depends on the
- * host arguments alone, so a warm call with the same bounds never grows it). */
+ * Scratch: the per-stream scratch buffer holds the parts of key ranges cut into chunks, head_dim + 2 floats for
+ * each chunk and row: seqs x heads x 16 rows when max_new x group <= 16 (group = q_heads / heads), else
+ * tokens x q_heads rows, and the former beside them (with chunks of their own) when group <= 16 and
+ * 2 x tokens <= seqs x max_new.  Rows and chunks depend on the host arguments alone, so a warm call with the
+ * same bounds never grows it. */
 fp8rt_status fp8_paged_attention(const void* q, fp8rt_dtype qt, int64_t tokens, int64_t q_heads, int64_t ldq,
                                  int64_t hdq, const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale,
                                  const float* v_scale, fp8rt_format f, int64_t pages, int64_t heads,
