@@ -222,7 +222,8 @@ __device__ __forceinline__ float reached(float lv) { return lv > -INFINITY ? fma
 // part in: m, l = sum 2^(t - m) and this lane's D/64 dimensions of sum 2^(t - m) v.  The matrix
 // kernels multiply a hidden key's value by a weight of 0, which is not 0 for a NaN or an infinity; they
 // notice such codes and scales and take this slow way for the rows concerned, after their loop
-// (inside it, it would cost the registers that keep the accumulators out of memory).
+// (inside it, it would cost the registers that keep the accumulators out of memory).  A row takes about 16 us
+// for 64 keys: with one NaN a prompt of 2048 tokens 17 ms instead of 0.16, two sequences of 131072 4 instead of 0.1.
 template <int F, int D>
 __device__ void careful_row(const AttendArgs& a, int64_t b, int32_t head, int64_t tok, int64_t qh, Range see, float& m,
                             float& l, float* y) {
