@@ -124,6 +124,22 @@ def lib():
         L.fp8_paged_attention.restype = C.c_int
         L.fp8_paged_attention.argtypes = [P, C.c_int, I64, I64, I64, I64, P, P, P, P, C.c_int, I64, I64, I64, I64, P,
                                           I64, I64, P, P, I64, I64, I64, F, I32, I64, P, C.c_int, I64, I64, P, P]
+        L.fp8_expert_route.restype = C.c_int
+        L.fp8_expert_route.argtypes = [P, C.c_int, I64, I64, I64, C.c_int, P, I64, I64, I64, I64, I32, F, P, P, P, P, P, P]
+        L.fp8_expert_route_backward.restype = C.c_int
+        L.fp8_expert_route_backward.argtypes = [P, C.c_int, I64, I64, I64, C.c_int, I64, I32, F, P, P, P, I64, P]
+        L.fp8_expert_gemm.restype = C.c_int
+        L.fp8_expert_gemm.argtypes = [P, C.c_int, I64, I64, Gran, P, P, I64, P, C.c_int, Gran, P, P, I64, I64, I64, I64, P,
+                                      C.c_int, I64, U32, P]
+        L.fp8_gated_quantize.restype = C.c_int
+        L.fp8_gated_quantize.argtypes = [P, C.c_int, I64, I64, I64, C.c_int, Gran, C.c_int, C.c_int, F, I32, P, P, P, I64,
+                                         P, C.c_int, I64, P, P, P, P]
+        L.fp8_gated_backward.restype = C.c_int
+        L.fp8_gated_backward.argtypes = [P, C.c_int, I64, I64, I64, P, C.c_int, I64, P, C.c_int, P, I64, P, I64, P, P]
+        L.fp8_expert_combine.restype = C.c_int
+        L.fp8_expert_combine.argtypes = [P, C.c_int, I64, I64, I64, P, P, I64, I64, P, I64, P, I64, P]
+        L.fp8_expert_combine_backward.restype = C.c_int
+        L.fp8_expert_combine_backward.argtypes = [P, C.c_int, I64, I64, I64, P, I64, I64, P, P, I64, P, I64, P, P]
         L.fp8_call_packed.restype = C.c_int
         L.fp8_call_packed.argtypes = [C.c_char_p, I64]
         _lib = L
@@ -522,7 +538,160 @@ def fp8_paged_attention(q, k_cache, v_cache, k_scale, v_scale, fmt, block_table,
         _dtype(y), sy[0], sy[1], 0 if lse is None else lse.data_ptr(), _stream(stream)))
 
 
-__all__ = ["fp8_rmsnorm_quantize", "fp8_rmsnorm_backward", "fp8_kv_append", "fp8_paged_attention",
+SOFTMAX, SIGMOID = 0, 1
+SILU, GELU = 0, 1
+KEPT_GROUP = 128  # columns of a group of a gated activation's checkpoint
+
+_ROUTE = struct.Struct("13qd6q")
+_ROUTE_GRAD = struct.Struct("9qd5q")
+_EXPERTS = struct.Struct("25q")
+_GATED = struct.Struct("11qd12q")
+_GATED_GRAD = struct.Struct("17q")
+_COMBINE = struct.Struct("15q")
+_COMBINE_GRAD = struct.Struct("16q")
+
+
+def _ints(name, t, shape):
+    if t.shape != shape or t.dtype is not torch.int32 or not t.is_contiguous():
+        raise ValueError("%s must be contiguous int32 %s" % (name, list(shape)))
+    return t.data_ptr()
+
+
+def _floats(name, t, shape):
+    if t.shape != shape or t.dtype is not torch.float32 or not t.is_contiguous():
+        raise ValueError("%s must be contiguous float32 %s" % (name, list(shape)))
+    return t.data_ptr()
+
+
+def _live(t):
+    if t is None:
+        return 0
+    if t.numel() != 1 or t.dtype is not torch.int32:
+        raise ValueError("live must be one int32")
+    return t.data_ptr()
+
+
+def fp8_expert_route(logits, ids, weights, slots=None, order=None, offsets=None, score=SOFTMAX, bias=None, groups=1,
+                     top_groups=1, group_best=1, renormalise=True, scale=1.0, stream=None):
+    """The k experts of each token (ids, weights: [tokens x k]) from the router's logits [tokens x experts], and
+    the plan that sorts the choices by expert: slots [tokens x k], order [tokens k], offsets [experts + 1]."""
+    tokens, experts, ld = _mat(logits)
+    shape = ids.shape
+    if len(shape) != 2 or shape[0] != tokens:
+        raise ValueError("ids must be [tokens x k]")
+    k = shape[1]
+    plan = (0, 0, 0)
+    if slots is not None or order is not None or offsets is not None:
+        if slots is None or order is None or offsets is None:
+            raise ValueError("slots, order and offsets are the plan: all three or none")
+        plan = (_ints("slots", slots, shape), _ints("order", order, (tokens * k,)),
+                _ints("offsets", offsets, (experts + 1,)))
+    _call("fp8_expert_route", _ROUTE.pack(
+        4, logits.data_ptr(), _dtype(logits), tokens, experts, max(ld, experts) if tokens == 1 else ld, score,
+        0 if bias is None else _vec("bias", bias, experts, torch.float32), groups, top_groups, group_best, k,
+        renormalise, scale, _ints("ids", ids, shape), _floats("weights", weights, shape), *plan, _stream(stream)))
+
+
+def fp8_expert_route_backward(logits, ids, dweights, dlogits, score=SOFTMAX, renormalise=True, scale=1.0, stream=None):
+    """dlogits, the gradient of fp8_expert_route's weights for its logits."""
+    tokens, experts, ld = _mat(logits)
+    shape = ids.shape
+    if len(shape) != 2 or shape[0] != tokens:
+        raise ValueError("ids must be [tokens x k]")
+    ldd = _rows("dlogits", dlogits, (tokens, experts), logits.dtype)
+    if tokens == 1:  # (one row: any stride)
+        ld, ldd = max(ld, experts), max(ldd, experts)
+    _call("fp8_expert_route_backward", _ROUTE_GRAD.pack(
+        5, logits.data_ptr(), _dtype(logits), tokens, experts, ld, score, shape[1], renormalise, scale,
+        _ints("ids", ids, shape), _floats("dweights", dweights, shape), dlogits.data_ptr(), ldd, _stream(stream)))
+
+
+def fp8_expert_gemm(a, fa, ga, scale_a, b, fb, gb, scale_b, offsets, y, order=None, choices=1, stream=None):
+    """y[s] = a[row] times the weights of the expert whose slots offsets[e] .. offsets[e + 1] - 1 hold s, with
+    row = order[s] // choices, or s without an order; b is the PackedWeights image of [experts N x K]."""
+    a_rows, K, lda = _mat(a)
+    slots, N, ldy = _mat(y)
+    experts = offsets.numel() - 1
+    if not isinstance(b, PackedWeights):
+        raise ValueError("b must be the PackedWeights image of the experts' weights (fp8_pack_weights16)")
+    if b.K != K or b.N != experts * N or experts < 1:
+        raise ValueError("b must hold [experts * N x K] codes")
+    if a.dtype is not torch.uint8:
+        raise ValueError("a must be uint8 codes")
+    _call("fp8_expert_gemm", _EXPERTS.pack(
+        6, a.data_ptr(), fa, a_rows, max(lda, K) if a_rows == 1 else lda, *ga,
+        _per_group("scale_a", scale_a, ngroups(a_rows, ga[0]) * ngroups(K, ga[1])),
+        0 if order is None else _ints("order", order, (slots,)), choices, b.data_ptr(), fb, *gb,
+        _per_group("scale_b", scale_b, ngroups(b.N, gb[0]) * ngroups(K, gb[1])),
+        _ints("offsets", offsets, (experts + 1,)), experts, slots, N, K, y.data_ptr(), _dtype(y),
+        max(ldy, N) if slots == 1 else ldy, B_PACKED16, _stream(stream)))
+
+
+def fp8_gated_quantize(x, gran, fmt, mode, eps, pow2_round_up, scale, q, act=SILU, inv_scale=None, amax_out=None,
+                       kept=None, kept_scale=None, kept_fmt=E4M3, live=None, stream=None):
+    """Codes q and scales of act(gate) * up, x = [gate | up] [rows x 2 cols]; kept and kept_scale
+    [rows x 2 x groups of 128] receive x as an 8-bit checkpoint; live: one int32, the rows that count."""
+    rows, both, ld = _mat(x)
+    cols = both // 2
+    if both != 2 * cols:
+        raise ValueError("x must have an even number of columns: the gates, then the ups")
+    gr, gc = gran
+    n = ngroups(rows, gr) * ngroups(cols, gc)
+    ldk = pk = ps = 0
+    if kept is not None or kept_scale is not None:
+        if kept is None or kept_scale is None:
+            raise ValueError("kept and kept_scale are given together")
+        ldk, pk = _rows("kept", kept, (rows, both), torch.uint8), kept.data_ptr()
+        ps = _floats("kept_scale", kept_scale, (rows, 2, -(-cols // KEPT_GROUP)))
+    _call("fp8_gated_quantize", _GATED.pack(
+        7, x.data_ptr(), _dtype(x), rows, cols, ld, act, gr, gc, fmt, mode, eps, pow2_round_up,
+        _per_group("scale", scale, n), 0 if inv_scale is None else _per_group("inv_scale", inv_scale, n),
+        q.data_ptr(), _rows("q", q, (rows, cols), torch.uint8), pk, kept_fmt, ldk, ps,
+        0 if amax_out is None else _per_group("amax_out", amax_out, n), _live(live), _stream(stream)))
+
+
+def fp8_gated_backward(dz, kept, kept_scale, dx, act=SILU, z=None, kept_fmt=E4M3, live=None, stream=None):
+    """dx [rows x 2 cols], the gradient of act(gate) * up, and z, that product again, from the 8-bit checkpoint."""
+    rows, cols, ld = _mat(dz)
+    both, dtype = (rows, 2 * cols), dz.dtype
+    _call("fp8_gated_backward", _GATED_GRAD.pack(
+        8, dz.data_ptr(), _dtype(dz), rows, cols, ld, kept.data_ptr(), kept_fmt, _rows("kept", kept, both, torch.uint8),
+        _floats("kept_scale", kept_scale, (rows, 2, -(-cols // KEPT_GROUP))), act, dx.data_ptr(),
+        _rows("dx", dx, both, dtype), 0 if z is None else z.data_ptr(),
+        0 if z is None else _rows("z", z, (rows, cols), dtype), _live(live), _stream(stream)))
+
+
+def fp8_expert_combine(x, slots, weights, y, residual=None, stream=None):
+    """y[t] = residual[t] + sum_j weights[t, j] x[slots[t, j]]; slots outside x count for nothing."""
+    x_rows, cols, ld = _mat(x)
+    shape = slots.shape
+    if len(shape) != 2:
+        raise ValueError("slots must be [tokens x k]")
+    tokens, k = shape
+    ldr = pr = 0
+    if residual is not None:
+        ldr, pr = _rows("residual", residual, (tokens, cols), x.dtype), residual.data_ptr()
+    _call("fp8_expert_combine", _COMBINE.pack(
+        9, x.data_ptr(), _dtype(x), x_rows, cols, ld, _ints("slots", slots, shape), _floats("weights", weights, shape),
+        tokens, k, pr, ldr, y.data_ptr(), _rows("y", y, (tokens, cols), x.dtype), _stream(stream)))
+
+
+def fp8_expert_combine_backward(dy, x, slots, weights, dx, dweights, stream=None):
+    """dx[slots[t, j]] = weights[t, j] dy[t] and dweights[t, j] = <dy[t], x[slots[t, j]]> of fp8_expert_combine."""
+    tokens, cols, ld = _mat(dy)
+    shape, dtype = slots.shape, dy.dtype
+    if len(shape) != 2 or shape[0] != tokens:
+        raise ValueError("slots must be [tokens x k]")
+    rows = x.shape[0]
+    _call("fp8_expert_combine_backward", _COMBINE_GRAD.pack(
+        10, dy.data_ptr(), _dtype(dy), tokens, cols, ld, x.data_ptr(), rows, _rows("x", x, (rows, cols), dtype),
+        _ints("slots", slots, shape), _floats("weights", weights, shape), shape[1], dx.data_ptr(),
+        _rows("dx", dx, (rows, cols), dtype), _floats("dweights", dweights, shape), _stream(stream)))
+
+
+__all__ = ["fp8_expert_route", "fp8_expert_route_backward", "fp8_expert_gemm", "fp8_gated_quantize", "fp8_gated_backward",
+           "fp8_expert_combine", "fp8_expert_combine_backward", "SOFTMAX", "SIGMOID", "SILU", "GELU", "KEPT_GROUP",
+           "fp8_rmsnorm_quantize", "fp8_rmsnorm_backward", "fp8_kv_append", "fp8_paged_attention",
            "fp8_pack_weights16", "fp8_quantize_packed16", "PackedWeights", "packed16_bytes", "B_PACKED16", "fp8_quant_error", "fp8_granularity_ledger", "LedgerSpec", "LedgerRow", "fp8_delayed_scale_update", "HIST_MAX", "HIST_LATEST", "fp8_weight_only_gemm", "fp8_scaled_gemm_fp8out", "fp8_amax", "fp8_compute_scale", "fp8_quantize", "fp8_quantize_transpose", "fp8_dequantize",
            "fp8_amax_history_update", "fp8_scaled_gemm", "lib", "raw_call", "Gran", "Fp8rtError",
            "E4M3", "E5M2", "F32", "BF16", "DYNAMIC", "GIVEN", "POW2_SCALES", "EXACT_PRODUCTS", "EXACT_AUTO_BYTES", "FMAX", "ngroups",

@@ -729,4 +729,258 @@ fp8rt_status fp8_paged_attention(const void* q, fp8rt_dtype qt, int64_t tokens, 
   return from_hip(launch_paged_attention(a, stream));
 }
 
+namespace {
+
+constexpr int64_t kInt31 = int64_t(1) << 31;
+
+// What routing and its gradient share.
+fp8rt_status route_setup(const void* logits, fp8rt_dtype lt, int64_t tokens, int64_t experts, int64_t ld,
+                         fp8rt_score score, int64_t k, int32_t renormalise, float scale, RouteArgs& a) {
+  if (!logits || !valid_dtype(lt) || (score != FP8RT_SOFTMAX && score != FP8RT_SIGMOID)) return FP8RT_EINVAL;
+  if (tokens <= 0 || experts <= 0 || k <= 0 || ld < experts || k > experts || !isfinite(scale)) return FP8RT_EINVAL;
+  if (experts > kRouteMaxExperts || k > kRouteMaxK) return FP8RT_EUNSUPPORTED;
+  if (tokens >= kInt31 || tokens * k >= kInt31 || ld >= kInt31) return FP8RT_EINVAL;
+  if (reinterpret_cast<uintptr_t>(logits) & (lt == FP8RT_F32 ? 3u : 1u)) return FP8RT_EALIGN;
+  a.logits = logits;
+  a.lt = lt;
+  a.tokens = tokens;
+  a.experts = static_cast<int>(experts);
+  a.ld = ld;
+  a.score = score;
+  a.k = static_cast<int>(k);
+  a.renormalise = renormalise != 0;
+  a.scale = scale;
+  return FP8RT_OK;
+}
+
+// What the weighted sum and its gradient share.
+fp8rt_status combine_setup(const void* x, fp8rt_dtype xt, int64_t x_rows, int64_t cols, int64_t ldx,
+                           const int32_t* slots, const float* weights, int64_t tokens, int64_t k, CombineArgs& a) {
+  if (!x || !valid_dtype(xt) || !slots || !weights) return FP8RT_EINVAL;
+  if (x_rows <= 0 || cols <= 0 || ldx < cols || tokens <= 0 || k <= 0) return FP8RT_EINVAL;
+  if (x_rows >= kInt31 || cols > kInt31 || tokens >= kInt31) return FP8RT_EINVAL;
+  if (k > kRouteMaxK) return FP8RT_EUNSUPPORTED;
+  if (cols % 8 != 0 || ldx % 8 != 0 || !aligned16(x) || !aligned4(slots) || !aligned4(weights)) return FP8RT_EALIGN;
+  a.x = x;
+  a.xt = xt;
+  a.x_rows = x_rows;
+  a.cols = cols;
+  a.ldx = ldx;
+  a.slots = slots;
+  a.weights = weights;
+  a.tokens = tokens;
+  a.k = static_cast<int>(k);
+  return FP8RT_OK;
+}
+
+}  // namespace
+
+fp8rt_status fp8_expert_route(const void* logits, fp8rt_dtype lt, int64_t tokens, int64_t experts, int64_t ld,
+                              fp8rt_score score, const float* bias, int64_t groups, int64_t top_groups,
+                              int64_t group_best, int64_t k, int32_t renormalise, float scale, int32_t* ids,
+                              float* weights, int32_t* slots, int32_t* order, int32_t* offsets, hipStream_t stream) {
+  RouteArgs a;
+  const fp8rt_status st = route_setup(logits, lt, tokens, experts, ld, score, k, renormalise, scale, a);
+  if (st != FP8RT_OK) return st;
+  if (!ids || !weights || !slots != !order || !slots != !offsets) return FP8RT_EINVAL;
+  if (groups <= 0 || top_groups <= 0 || top_groups > groups || (group_best != 1 && group_best != 2))
+    return FP8RT_EINVAL;
+  if (groups > kRouteMaxGroups) return FP8RT_EUNSUPPORTED;
+  if (experts % groups != 0 || k > experts / groups * top_groups) return FP8RT_EINVAL;
+  if (!aligned4(ids) || !aligned4(weights) || (bias && !aligned4(bias)) || !aligned4(slots) || !aligned4(order) ||
+      !aligned4(offsets))
+    return FP8RT_EALIGN;
+  a.bias = bias;
+  a.groups = static_cast<int>(groups);
+  a.top_groups = static_cast<int>(top_groups);
+  a.group_best = static_cast<int>(group_best);
+  a.ids = ids;
+  a.weights = weights;
+  a.slots = slots;
+  a.order = order;
+  a.offsets = offsets;
+  return from_hip(launch_expert_route(a, stream));
+}
+
+fp8rt_status fp8_expert_route_backward(const void* logits, fp8rt_dtype lt, int64_t tokens, int64_t experts,
+                                       int64_t ld, fp8rt_score score, int64_t k, int32_t renormalise, float scale,
+                                       const int32_t* ids, const float* dweights, void* dlogits, int64_t lddl,
+                                       hipStream_t stream) {
+  RouteArgs a;
+  const fp8rt_status st = route_setup(logits, lt, tokens, experts, ld, score, k, renormalise, scale, a);
+  if (st != FP8RT_OK) return st;
+  if (!ids || !dweights || !dlogits || lddl < experts || lddl >= kInt31) return FP8RT_EINVAL;
+  if (dlogits == logits && lddl != ld) return FP8RT_EINVAL;
+  if (!aligned4(ids) || !aligned4(dweights) || (reinterpret_cast<uintptr_t>(dlogits) & (lt == FP8RT_F32 ? 3u : 1u)))
+    return FP8RT_EALIGN;
+  a.ids = const_cast<int32_t*>(ids);
+  a.dweights = dweights;
+  a.dlogits = dlogits;
+  a.lddl = lddl;
+  return from_hip(launch_expert_route_backward(a, stream));
+}
+
+fp8rt_status fp8_expert_gemm(const uint8_t* a, fp8rt_format fa, int64_t a_rows, int64_t lda, fp8rt_gran ga,
+                             const float* scale_a, const int32_t* order, int64_t choices, const uint8_t* b,
+                             fp8rt_format fb, fp8rt_gran gb, const float* scale_b, const int32_t* offsets,
+                             int64_t experts, int64_t slots, int64_t N, int64_t K, void* y, fp8rt_dtype yt,
+                             int64_t ldy, uint32_t flags, hipStream_t stream) {
+  if (!a || !scale_a || !b || !scale_b || !offsets || !y || !valid_fmt(fa) || !valid_fmt(fb) || !valid_dtype(yt))
+    return FP8RT_EINVAL;
+  if (flags & ~static_cast<uint32_t>(FP8RT_B_PACKED16)) return FP8RT_EINVAL;
+  if (a_rows <= 0 || experts <= 0 || slots <= 0 || N <= 0 || K <= 0 || lda < K || ldy < N || choices <= 0)
+    return FP8RT_EINVAL;
+  if (ga.rows < 0 || ga.cols < 0 || gb.rows < 0 || gb.cols < 0) return FP8RT_EINVAL;
+  if (a_rows >= kInt31 || slots >= kInt31 || choices >= kInt31 || N >= kInt31 || lda >= kInt31 || ldy >= kInt31)
+    return FP8RT_EINVAL;
+  if (!(flags & FP8RT_B_PACKED16) || fb != FP8RT_E4M3) return FP8RT_EUNSUPPORTED;
+  if (experts > kRouteMaxExperts || K > (int64_t(1) << 20) || a_rows * lda >= (int64_t(1) << 32)) return FP8RT_EUNSUPPORTED;
+  if ((slots / 16 + std::min(experts, slots) + 1) * (N / 64 + 1) > (int64_t(1) << 23)) return FP8RT_EUNSUPPORTED;
+  if (N % 16 != 0 || K % 128 != 0 || lda % 16 != 0 || ldy % (yt == FP8RT_BF16 ? 8 : 4) != 0) return FP8RT_EALIGN;
+  if (!aligned16(a) || !aligned16(b) || !aligned16(y) || !aligned4(scale_a) || !aligned4(scale_b) ||
+      !aligned4(offsets) || !aligned4(order))
+    return FP8RT_EALIGN;
+  if (group_extent(K, ga.cols) != K || group_extent(K, gb.cols) != K) return FP8RT_EUNSUPPORTED;
+  ExpertGemmArgs g;
+  const int64_t era = group_extent(a_rows, ga.rows), erb = group_extent(experts * N, gb.rows);
+  if (era != 1 && era != a_rows) return FP8RT_EUNSUPPORTED;
+  if (erb == 1) {
+    g.sb_expert = N;
+    g.sb_col = 1;
+  } else if (erb == N) {
+    g.sb_expert = 1;
+  } else if (erb != experts * N) {
+    return FP8RT_EUNSUPPORTED;
+  }
+  g.a = a;
+  g.fa = fa;
+  g.a_rows = a_rows;
+  g.lda = lda;
+  g.sa = scale_a;
+  g.sa_rows = era == 1;
+  g.order = order;
+  g.choices = choices;
+  g.b = b;
+  g.sb = scale_b;
+  g.offsets = offsets;
+  g.experts = experts;
+  g.slots = slots;
+  g.N = N;
+  g.K = K;
+  g.y = y;
+  g.yt = yt;
+  g.ldy = ldy;
+  return from_hip(launch_expert_gemm(g, stream));
+}
+
+fp8rt_status fp8_gated_quantize(const void* x, fp8rt_dtype xt, int64_t rows, int64_t cols, int64_t ldx, fp8rt_act act,
+                                fp8rt_gran g, fp8rt_format f, fp8rt_mode mode, float eps, int32_t pow2_round_up,
+                                float* scale, float* inv_scale, uint8_t* q, int64_t ldq, uint8_t* kept,
+                                fp8rt_format kf, int64_t ldk, float* kept_scale, float* amax_out, const int32_t* live,
+                                hipStream_t stream) {
+  if (!valid_dtype(xt) || !valid_fmt(f) || !valid_fmt(kf) || !scale || !q || !kept != !kept_scale) return FP8RT_EINVAL;
+  if (act != FP8RT_SILU && act != FP8RT_GELU) return FP8RT_EINVAL;
+  if (mode != FP8RT_DYNAMIC && mode != FP8RT_GIVEN) return FP8RT_EINVAL;
+  if ((mode == FP8RT_DYNAMIC || kept) && !valid_eps(eps)) return FP8RT_EINVAL;
+  const fp8rt_status st = check_matrix(x, rows, cols, ldx, g);
+  if (st != FP8RT_OK) return st;
+  if (ldx < 2 * cols || ldq < cols || (kept && ldk < 2 * cols)) return FP8RT_EINVAL;
+  if (ldq % 16 != 0 || (kept && ldk % 16 != 0) || !aligned16(q) || !aligned16(kept)) return FP8RT_EALIGN;
+  if (!aligned4(scale) || !aligned4(inv_scale) || !aligned4(kept_scale) || !aligned4(amax_out) || !aligned4(live))
+    return FP8RT_EALIGN;
+  if (cols > kGatedMaxCols) return FP8RT_EUNSUPPORTED;
+  GatedArgs a;
+  a.er = group_extent(rows, g.rows);
+  a.ec = group_extent(cols, g.cols);
+  if (a.er != 1) {
+    if (a.er != rows || a.ec != cols || mode != FP8RT_GIVEN) return FP8RT_EUNSUPPORTED;
+  } else if (a.ec != cols && ((a.ec & (a.ec - 1)) != 0 || a.ec > 512)) {
+    return FP8RT_EUNSUPPORTED;
+  }
+  a.x = x;
+  a.xt = xt;
+  a.rows = rows;
+  a.cols = cols;
+  a.ldx = ldx;
+  a.act = act;
+  a.fmt = f;
+  a.mode = mode;
+  a.eps = mode == FP8RT_DYNAMIC || kept ? eps : 1.0f;
+  a.pow2 = pow2_round_up != 0;
+  a.scale = scale;
+  a.inv_scale = inv_scale;
+  a.q = q;
+  a.ldq = ldq;
+  a.kept = kept;
+  a.kf = kf;
+  a.ldk = ldk;
+  a.kept_scale = kept_scale;
+  a.amax_out = amax_out;
+  a.live = live;
+  return from_hip(launch_gated_quantize(a, stream));
+}
+
+fp8rt_status fp8_gated_backward(const void* dz, fp8rt_dtype t, int64_t rows, int64_t cols, int64_t lddz,
+                                const uint8_t* kept, fp8rt_format kf, int64_t ldk, const float* kept_scale,
+                                fp8rt_act act, void* dx, int64_t lddx, void* z, int64_t ldz, const int32_t* live,
+                                hipStream_t stream) {
+  if (!valid_dtype(t) || !valid_fmt(kf) || !kept || !kept_scale || !dx) return FP8RT_EINVAL;
+  if (act != FP8RT_SILU && act != FP8RT_GELU) return FP8RT_EINVAL;
+  const fp8rt_status st = check_matrix(dz, rows, cols, lddz, fp8rt_gran{1, 0});
+  if (st != FP8RT_OK) return st;
+  if (ldk < 2 * cols || lddx < 2 * cols || (z && ldz < cols)) return FP8RT_EINVAL;
+  if (ldk % 16 != 0 || lddx % 16 != 0 || (z && ldz % 16 != 0)) return FP8RT_EALIGN;
+  if (!aligned16(kept) || !aligned16(dx) || !aligned16(z) || !aligned4(kept_scale) || !aligned4(live))
+    return FP8RT_EALIGN;
+  GatedArgs a;
+  a.x = dz;
+  a.xt = t;
+  a.rows = rows;
+  a.cols = cols;
+  a.ldx = lddz;
+  a.act = act;
+  a.kept = const_cast<uint8_t*>(kept);
+  a.kf = kf;
+  a.ldk = ldk;
+  a.kept_scale = const_cast<float*>(kept_scale);
+  a.dx = dx;
+  a.lddx = lddx;
+  a.z = z;
+  a.ldz = ldz;
+  a.live = live;
+  return from_hip(launch_gated_backward(a, stream));
+}
+
+fp8rt_status fp8_expert_combine(const void* x, fp8rt_dtype xt, int64_t x_rows, int64_t cols, int64_t ldx,
+                                const int32_t* slots, const float* weights, int64_t tokens, int64_t k,
+                                const void* residual, int64_t ldr, void* y, int64_t ldy, hipStream_t stream) {
+  CombineArgs a;
+  const fp8rt_status st = combine_setup(x, xt, x_rows, cols, ldx, slots, weights, tokens, k, a);
+  if (st != FP8RT_OK) return st;
+  if (!y || y == x || ldy < cols || (residual && ldr < cols) || (y == residual && ldy != ldr)) return FP8RT_EINVAL;
+  if (ldy % 8 != 0 || (residual && ldr % 8 != 0) || !aligned16(y) || !aligned16(residual)) return FP8RT_EALIGN;
+  a.res = residual;
+  a.ldr = ldr;
+  a.y = y;
+  a.ldy = ldy;
+  return from_hip(launch_expert_combine(a, stream));
+}
+
+fp8rt_status fp8_expert_combine_backward(const void* dy, fp8rt_dtype xt, int64_t tokens, int64_t cols, int64_t lddy,
+                                         const void* x, int64_t x_rows, int64_t ldx, const int32_t* slots,
+                                         const float* weights, int64_t k, void* dx, int64_t lddx, float* dweights,
+                                         hipStream_t stream) {
+  CombineArgs a;
+  const fp8rt_status st = combine_setup(x, xt, x_rows, cols, ldx, slots, weights, tokens, k, a);
+  if (st != FP8RT_OK) return st;
+  if (!dy || !dx || !dweights || dx == dy || lddy < cols || lddx < cols || (dx == x && lddx != ldx)) return FP8RT_EINVAL;
+  if (lddy % 8 != 0 || lddx % 8 != 0 || !aligned16(dy) || !aligned16(dx) || !aligned4(dweights)) return FP8RT_EALIGN;
+  a.dy = dy;
+  a.lddy = lddy;
+  a.dx = dx;
+  a.lddx = lddx;
+  a.dw = dweights;
+  return from_hip(launch_expert_combine_backward(a, stream));
+}
+
 }  // extern "C"

@@ -135,6 +135,36 @@ template <> struct Octet<float> {
   }
 };
 
+template <typename T>
+__device__ __forceinline__ void widen(const Octet<T>& o, float* out) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) out[i] = o.get(i);
+}
+
+// Two binary32 values rounded to nearest even onto bf16 (NaN stays NaN).
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  bf16x2 v;
+  v[0] = static_cast<__bf16>(a);
+  v[1] = static_cast<__bf16>(b);
+  return __builtin_bit_cast(uint32_t, v);
+}
+
+__device__ __forceinline__ void store8(uint16_t* p, const float* v) {
+  *reinterpret_cast<u32x4*>(p) =
+      u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+}
+__device__ __forceinline__ void store8(float* p, const float* v) {
+  u32x4 a, b;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    a[i] = __float_as_uint(v[i]);
+    b[i] = __float_as_uint(v[i + 4]);
+  }
+  reinterpret_cast<u32x4*>(p)[0] = a;
+  reinterpret_cast<u32x4*>(p)[1] = b;
+}
+
 // ---------------------------------------------------------------------------
 // FP32 -> FP8 for 4 values, byte i of the result = code of value i.
 // The clamp to +-F_max comes first, so the convert never sees an overflow;

@@ -300,4 +300,100 @@ struct AttendArgs {
 };
 hipError_t launch_paged_attention(const AttendArgs& a, hipStream_t stream);
 
+// Routing to experts, their weighted sum, and the gradients (expert_route.hip, expert_combine.hip).
+struct RouteArgs {
+  const void* logits = nullptr;  // type lt
+  int lt = 0;
+  int64_t tokens = 0;
+  int experts = 0;
+  int64_t ld = 0;
+  int score = 0;
+  const float* bias = nullptr;
+  int groups = 1, top_groups = 1, group_best = 1, k = 1;
+  int renormalise = 0;
+  float scale = 1.0f;
+  int32_t* ids = nullptr;
+  float* weights = nullptr;
+  int32_t* slots = nullptr;  // the plan: all three or none
+  int32_t* order = nullptr;
+  int32_t* offsets = nullptr;
+  const float* dweights = nullptr;  // backward: ids are read
+  void* dlogits = nullptr;
+  int64_t lddl = 0;
+};
+constexpr int64_t kRouteMaxExperts = 1024, kRouteMaxK = 32, kRouteMaxGroups = 64;
+hipError_t launch_expert_route(const RouteArgs& a, hipStream_t stream);
+hipError_t launch_expert_route_backward(const RouteArgs& a, hipStream_t stream);
+
+struct CombineArgs {
+  const void* x = nullptr;  // type xt
+  int xt = 0;
+  int64_t x_rows = 0, cols = 0, ldx = 0;
+  const int32_t* slots = nullptr;
+  const float* weights = nullptr;
+  int64_t tokens = 0;
+  int k = 1;
+  const void* res = nullptr;
+  int64_t ldr = 0;
+  void* y = nullptr;
+  int64_t ldy = 0;
+  const void* dy = nullptr;  // backward
+  int64_t lddy = 0;
+  void* dx = nullptr;
+  int64_t lddx = 0;
+  float* dw = nullptr;
+};
+hipError_t launch_expert_combine(const CombineArgs& a, hipStream_t stream);
+hipError_t launch_expert_combine_backward(const CombineArgs& a, hipStream_t stream);
+
+// The experts' scaled products over a weight image (expert_gemm.hip).
+struct ExpertGemmArgs {
+  const uint8_t* a = nullptr;
+  int fa = 0;
+  int64_t a_rows = 0, lda = 0;
+  const float* sa = nullptr;
+  bool sa_rows = true;  // a scale per row, else one
+  const int32_t* order = nullptr;
+  int64_t choices = 1;
+  const uint8_t* b = nullptr;  // image of [experts N x K]
+  const float* sb = nullptr;
+  int64_t sb_expert = 0, sb_col = 0;  // strides of the scale from expert to expert and column to column
+  const int32_t* offsets = nullptr;
+  int64_t experts = 0, slots = 0, N = 0, K = 0;
+  void* y = nullptr;
+  int yt = 0;
+  int64_t ldy = 0;
+};
+hipError_t launch_expert_gemm(const ExpertGemmArgs& g, hipStream_t stream);
+
+// Gated activation to FP8 with a checkpoint, and its gradient (gated.hip).
+struct GatedArgs {
+  const void* x = nullptr;  // type xt; backward: dz
+  int xt = 0;
+  int64_t rows = 0, cols = 0, ldx = 0;
+  int act = 0;
+  int64_t er = 1, ec = 0;  // effective group extents, as NormArgs
+  int fmt = 0, mode = 0;
+  float eps = 1.0f;
+  int pow2 = 0;
+  float* scale = nullptr;
+  float* inv_scale = nullptr;
+  uint8_t* q = nullptr;
+  int64_t ldq = 0;
+  uint8_t* kept = nullptr;  // nullable
+  int kf = 0;
+  int64_t ldk = 0;
+  float* kept_scale = nullptr;
+  float* amax_out = nullptr;
+  const int32_t* live = nullptr;
+  void* dx = nullptr;  // backward
+  int64_t lddx = 0;
+  void* z = nullptr;
+  int64_t ldz = 0;
+};
+constexpr int64_t kGatedMaxCols = 65536;  // 1024 threads take a row, 64 elements each
+constexpr int kKeptGroup = 128;           // columns of a checkpoint's group
+hipError_t launch_gated_quantize(const GatedArgs& a, hipStream_t stream);
+hipError_t launch_gated_backward(const GatedArgs& a, hipStream_t stream);
+
 }  // namespace fp8rt

@@ -31,7 +31,7 @@ struct Words {
       return fp8rt_gran{rows, next<int32_t>()};
     } else if constexpr (sizeof(T) == 8) {
       return static_cast<T>(*w++);
-    } else {  // int32_t and the enumerations
+    } else {  // int32_t, uint32_t and the enumerations
       const int64_t x = *w++;
       ok = ok && x >= INT32_MIN && x <= INT32_MAX;
       return static_cast<T>(static_cast<int32_t>(x));
@@ -61,6 +61,13 @@ extern "C" fp8rt_status fp8_call_packed(const int64_t* words, int64_t n) {
     case FP8RT_CALL_RMSNORM_BACKWARD: return call(fp8_rmsnorm_backward, words, n);
     case FP8RT_CALL_KV_APPEND: return call(fp8_kv_append, words, n);
     case FP8RT_CALL_PAGED_ATTENTION: return call(fp8_paged_attention, words, n);
+    case FP8RT_CALL_EXPERT_ROUTE: return call(fp8_expert_route, words, n);
+    case FP8RT_CALL_EXPERT_ROUTE_BACKWARD: return call(fp8_expert_route_backward, words, n);
+    case FP8RT_CALL_EXPERT_GEMM: return call(fp8_expert_gemm, words, n);
+    case FP8RT_CALL_GATED_QUANTIZE: return call(fp8_gated_quantize, words, n);
+    case FP8RT_CALL_GATED_BACKWARD: return call(fp8_gated_backward, words, n);
+    case FP8RT_CALL_EXPERT_COMBINE: return call(fp8_expert_combine, words, n);
+    case FP8RT_CALL_EXPERT_COMBINE_BACKWARD: return call(fp8_expert_combine_backward, words, n);
   }
   return FP8RT_EINVAL;
 }

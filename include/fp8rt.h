@@ -567,7 +567,144 @@ fp8rt_status fp8_paged_attention(const void* q, fp8rt_dtype qt, int64_t tokens, 
                                  int64_t max_kv, float sm_scale, int32_t causal, int64_t window, void* y,
                                  fp8rt_dtype yt, int64_t ldy, int64_t hdy, float* lse, hipStream_t stream);
 
-/* The four calls above with their arguments as 64-bit words, for bindings that pay for every
+/* ---------------------------------------------------------------------------
+ * The gated half of a decoder layer, dense or with experts.  A dense layer runs
+ * scaled GEMM (gate and up) -> fp8_gated_quantize -> scaled GEMM (down); one with experts
+ *   fp8_expert_route -> fp8_expert_gemm (rows gathered) -> fp8_gated_quantize ->
+ *   fp8_expert_gemm -> fp8_expert_combine,
+ * without a copy to the host: the plan that the router writes stays on the device. */
+
+typedef FP8RT_ENUM(fp8rt_score) { FP8RT_SOFTMAX = 0, FP8RT_SIGMOID = 1 } fp8rt_score;
+
+/* The activation of a gate: g / (1 + e^-g), or g / (1 + e^-v) with v = 2 sqrt(2 / pi) (g + 0.044715 g^3)
+ * (the tanh form of GELU). */
+typedef FP8RT_ENUM(fp8rt_act) { FP8RT_SILU = 0, FP8RT_GELU = 1 } fp8rt_act;
+
+/* Routing: the k experts of each token, their weights, and the plan that sorts the
+ * choices by expert.  For token t, over its experts e:
+ *   p[e] = softmax(logits[t])[e] or 1 / (1 + e^-logits[t,e])
+ *   an expert whose logit is -Inf or NaN is absent: p = 0, and it is never chosen (+Inf counts as the
+ *   largest finite value)
+ *   key[e] = p[e] + bias[e], or without a bias the logit itself
+ *   groups > 1: the experts form `groups` runs of experts / groups; a run's score is its largest key
+ *     (group_best 1) or the sum of its two largest p[e] (+ bias[e]) (group_best 2; the one alone if
+ *     it has no second); the top_groups best runs stay (ties to the lower run)
+ *   ids[t,:]     the k largest keys of the runs that stay, in falling order, ties to the lower expert
+ *   weights[t,j] = scale p[ids[t,j]], divided by the sum of the chosen p if renormalise
+ * Keys with a bias and sums of two are formed and compared in binary64 (a binary32 score would choose
+ * differently at a border); weights are binary32.  A place that finds no expert (fewer than k
+ * present) has id -1, weight 0 and slot -1.
+ *   logits : [tokens x experts] fp32 / bf16 (lt), leading dimension ld;  bias : nullable [experts] fp32
+ *   ids, weights, slots : [tokens][k] int32, fp32, int32
+ * The plan (slots, order, offsets: all three, or all NULL): the choices in the order of expert, then token.
+ *   offsets : int32 [experts + 1]; expert e has slots offsets[e] .. offsets[e+1] - 1
+ *   order   : int32 [tokens * k]; slot s holds choice order[s] = t k + j; entries from
+ *             offsets[experts] on are left as they were
+ *   slots   : slots[t,j], the slot of that choice
+ * experts <= 1024, k <= 32, groups <= 64 (else FP8RT_EUNSUPPORTED); groups divides experts; k <= experts / groups *
+ * top_groups; tokens * k < 2^31; scale finite.  Alignment: pointers to their element.
+ * Scratch: the per-stream scratch buffer holds experts bytes for each 32 tokens. */
+fp8rt_status fp8_expert_route(const void* logits, fp8rt_dtype lt, int64_t tokens, int64_t experts, int64_t ld,
+                              fp8rt_score score, const float* bias, int64_t groups, int64_t top_groups,
+                              int64_t group_best, int64_t k, int32_t renormalise, float scale, int32_t* ids,
+                              float* weights, int32_t* slots, int32_t* order, int32_t* offsets, hipStream_t stream);
+
+/* Gradient of the weights for the logits (the choice itself has none):
+ *   with g[e] = scale dweights[t,j] at e = ids[t,j], 0 elsewhere; P = sum of the chosen p
+ *   renormalise: g[e] <- (g[e] - sum_i g[i] p[i] / P) / P over the chosen
+ *   softmax: dlogits[t,e] = p[e] (g[e] - sum_i g[i] p[i]);  sigmoid: g[e] p[e] (1 - p[e])
+ *   dlogits : [tokens x experts] of type lt (lddl), OVERWRITTEN; it may be logits itself (same leading dimension)
+ * An id outside [0, experts) counts for nothing; an id may stand once in a row.  Limits as
+ * fp8_expert_route. */
+fp8rt_status fp8_expert_route_backward(const void* logits, fp8rt_dtype lt, int64_t tokens, int64_t experts,
+                                       int64_t ld, fp8rt_score score, int64_t k, int32_t renormalise, float scale,
+                                       const int32_t* ids, const float* dweights, void* dlogits, int64_t lddl,
+                                       hipStream_t stream);
+
+/* The experts' scaled products: slot s, of the expert e with offsets[e] <= s < offsets[e+1], is
+ *   y[s,n] = s_a(r) s_b(e,n) sum_k dec(a[r,k]) dec(b[e,n,k]),   r = order[s] / choices, or s if order is NULL
+ * with the FP8 matrix cores' products and FP32 accumulation of fp8_scaled_gemm.
+ *   a  : [a_rows x K] codes (lda), format fa, scales scale_a with granularity ga
+ *   b  : the experts' weights [experts N x K] as one fp8_pack_weights16 image (fp8_quantize_packed16
+ *        writes it), format fb; scales scale_b with granularity gb of that matrix
+ *   offsets : int32 [experts + 1] on the device;  order : nullable int32 [slots] on the device
+ *   slots : rows of y (and entries of order), a bound on offsets[experts]
+ *   y  : [slots x N] bf16 / fp32 (ldy); rows of no expert are left as they were
+ * The device's integers are not trusted: offsets are clamped to [0, slots], an expert whose end lies before its
+ * start has no slots, and of two experts that claim one slot either may write it; a slot whose r lies outside
+ * [0, a_rows) is 0.
+ * Format pairs: E4M3 x E4M3 and E5M2 x E4M3 (a data gradient: the same call with the K-major weights).
+ * Granularities: ga row {1,0} or tensor {0,0}; gb channel {1,0}, expert {N,0} or tensor {0,0}; else
+ * FP8RT_EUNSUPPORTED.  flags: FP8RT_B_PACKED16, which is required (without it FP8RT_EUNSUPPORTED: decode and
+ * prompts share the one layout); other bits FP8RT_EINVAL.
+ * experts <= 1024, K <= 2^20, a_rows lda < 2^32 and at most 2^23 tiles of 16 rows by 64 columns (else
+ * FP8RT_EUNSUPPORTED); slots < 2^31.  Alignment: N a multiple of 16, K of 128, lda of 16, a and b 16-byte aligned; ldy a
+ * multiple of 8 (bf16) or 4 (fp32) and y 16-byte aligned. */
+fp8rt_status fp8_expert_gemm(const uint8_t* a, fp8rt_format fa, int64_t a_rows, int64_t lda, fp8rt_gran ga,
+                             const float* scale_a, const int32_t* order, int64_t choices, const uint8_t* b,
+                             fp8rt_format fb, fp8rt_gran gb, const float* scale_b, const int32_t* offsets,
+                             int64_t experts, int64_t slots, int64_t N, int64_t K, void* y, fp8rt_dtype yt,
+                             int64_t ldy, uint32_t flags, hipStream_t stream);
+
+/* Gated activation with an FP8 output: the operand of the down projection in one pass
+ * over the output of the gate and up projection.
+ *   z[i,j] = act(x[i,j]) x[i,cols+j]             (binary32)
+ *   q, scale, inv_scale = fp8_quantize(z, g, f, mode, eps, pow2_round_up)
+ *   x    : [rows x 2 cols] fp32 / bf16 (ldx): the gates, then the ups
+ *   kept, kept_scale : nullable (both or neither): x as an 8-bit checkpoint for fp8_gated_backward, each half
+ *          quantized in groups of 128 columns (the last one short): codes [rows x 2 cols] of format kf (ldk) and
+ *          scales fp32 [rows][2][ceil(cols / 128)], DYNAMIC with the same eps (which has to be valid then) and no
+ *          power-of-two rounding
+ *   amax_out : nullable, the observed max |z| of each group (for delayed scaling)
+ *   live : nullable int32 on the device: rows from live[0] on are left as they were in every output (the
+ *          offsets[experts] of a plan: fewer choices than places)
+ * Granularities, modes and non-finite data as fp8_rmsnorm_quantize: rows {1,0}; groups {1,g}, g = 16 .. 512
+ * a power of two; the whole tensor {0,0} with FP8RT_GIVEN only.
+ * Alignment as fp8_quantize.  cols <= 65536, else FP8RT_EUNSUPPORTED.
+ * Workspace: the per-stream workspace holds the amax partials of the {0,0} case. */
+fp8rt_status fp8_gated_quantize(const void* x, fp8rt_dtype xt, int64_t rows, int64_t cols, int64_t ldx, fp8rt_act act,
+                                fp8rt_gran g, fp8rt_format f, fp8rt_mode mode, float eps, int32_t pow2_round_up,
+                                float* scale, float* inv_scale, uint8_t* q, int64_t ldq, uint8_t* kept,
+                                fp8rt_format kf, int64_t ldk, float* kept_scale, float* amax_out, const int32_t* live,
+                                hipStream_t stream);
+
+/* Gradient of z = act(g) u from the checkpoint (the casts count as the identity).  With g, u the
+ * values that kept's codes stand for (fl32(scale dec(code))):
+ *   dx[i,j] = dz[i,j] u act'(g),  dx[i,cols+j] = dz[i,j] act(g),  z[i,j] = act(g) u
+ *   dz : [rows x cols] fp32 / bf16 (t, lddz);  dx : [rows x 2 cols] of type t (lddx)
+ *   z  : nullable [rows x cols] of type t (ldz): the activation computed again, for the down projection's weight
+ *        gradient
+ *   kept, kf, ldk, kept_scale, live : as fp8_gated_quantize
+ * Alignment: cols and leading dimensions multiples of 16, matrices 16-byte aligned. */
+fp8rt_status fp8_gated_backward(const void* dz, fp8rt_dtype t, int64_t rows, int64_t cols, int64_t lddz,
+                                const uint8_t* kept, fp8rt_format kf, int64_t ldk, const float* kept_scale,
+                                fp8rt_act act, void* dx, int64_t lddx, void* z, int64_t ldz, const int32_t* live,
+                                hipStream_t stream);
+
+/* The sum over a token's experts:
+ *   y[t,:] = residual[t,:] + sum_j weights[t,j] x[slots[t,j],:]    (binary32, j rising, rounded once)
+ *   x : [x_rows x cols] fp32 / bf16 (xt, ldx);  slots, weights : [tokens][k] int32, fp32
+ *   residual : nullable [tokens x cols] of type xt (ldr);  y : [tokens x cols] of type xt (ldy)
+ * A slot outside [0, x_rows) counts for nothing, whatever its weight.  y may be residual itself (same
+ * leading dimension).  k <= 32 (else FP8RT_EUNSUPPORTED).
+ * Alignment: cols and leading dimensions multiples of 8, matrices 16-byte aligned. */
+fp8rt_status fp8_expert_combine(const void* x, fp8rt_dtype xt, int64_t x_rows, int64_t cols, int64_t ldx,
+                                const int32_t* slots, const float* weights, int64_t tokens, int64_t k,
+                                const void* residual, int64_t ldr, void* y, int64_t ldy, hipStream_t stream);
+
+/* Its gradient (that of residual is dy itself):
+ *   dx[slots[t,j],:] = weights[t,j] dy[t,:],   dweights[t,j] = sum_c dy[t,c] x[slots[t,j],c]
+ *   dy : [tokens x cols] of type xt (lddy);  dx : [x_rows x cols] of type xt (lddx): rows of no slot are left
+ *        as they were;  dweights : [tokens][k] fp32, 0 where the slot is outside [0, x_rows)
+ * Slots are distinct (as the router's are): of two choices with one slot either may write dx's
+ * row.  dx may be x itself (same leading dimension).  Sums are binary32 in a fixed order.  Limits and
+ * alignment as fp8_expert_combine. */
+fp8rt_status fp8_expert_combine_backward(const void* dy, fp8rt_dtype xt, int64_t tokens, int64_t cols, int64_t lddy,
+                                         const void* x, int64_t x_rows, int64_t ldx, const int32_t* slots,
+                                         const float* weights, int64_t k, void* dx, int64_t lddx, float* dweights,
+                                         hipStream_t stream);
+
+/* The calls of a decoder layer with their arguments as 64-bit words, for bindings that pay for every
  * argument they convert (31 arguments through a foreign-function interface can cost more than the
  * smallest of these kernels).
  *   words[0]    : the call (fp8rt_call)
@@ -580,7 +717,14 @@ typedef FP8RT_ENUM(fp8rt_call) {
   FP8RT_CALL_RMSNORM_QUANTIZE = 0,
   FP8RT_CALL_RMSNORM_BACKWARD = 1,
   FP8RT_CALL_KV_APPEND = 2,
-  FP8RT_CALL_PAGED_ATTENTION = 3
+  FP8RT_CALL_PAGED_ATTENTION = 3,
+  FP8RT_CALL_EXPERT_ROUTE = 4,
+  FP8RT_CALL_EXPERT_ROUTE_BACKWARD = 5,
+  FP8RT_CALL_EXPERT_GEMM = 6,
+  FP8RT_CALL_GATED_QUANTIZE = 7,
+  FP8RT_CALL_GATED_BACKWARD = 8,
+  FP8RT_CALL_EXPERT_COMBINE = 9,
+  FP8RT_CALL_EXPERT_COMBINE_BACKWARD = 10
 } fp8rt_call;
 fp8rt_status fp8_call_packed(const int64_t* words, int64_t n);
 
