@@ -2,18 +2,16 @@
 // router's plan, against each expert's FP8 weights (one fragment-ordered image).
 //
 //   y[s,n] = s_a(r) s_b(e,n) sum_k dec(a[r,k]) dec(b[e,n,k]),   offsets[e] <= s < offsets[e+1]
+#include <stdlib.h>
+
 #include <algorithm>
 
-#include "device_common.h"
+#include "gemm_tile.h"
 #include "internal.h"
 
 namespace fp8rt {
 
 namespace {
-
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 
 // A tile of up to TM consecutive slots of one expert.
 struct Tile {
@@ -55,6 +53,50 @@ __device__ __forceinline__ bool find_tile(const ExpertGemmArgs& g, int index, Ti
       return true;
     }
     before += __builtin_amdgcn_readlane(s, 63);
+  }
+  return false;
+}
+
+// Work unit of workgroup b of the tile kernel: (row tile, column tile).  Experts one after the other; inside an expert
+// groups of 4 row tiles go through the column tiles together; each XCD (workgroups are dealt to the 8 in turn) gets a
+// contiguous range of that order, so that its L2 serves what neighbours share.  False past the last.
+__device__ __forceinline__ bool find_unit(const ExpertGemmArgs& g, int b, int col_tiles, Tile& t, int& col) {
+  const int lane = threadIdx.x & 63, E = static_cast<int>(g.experts);
+  int units = 0;
+  for (int e = lane; e < E; e += 64) {
+    int lo, hi;
+    expert_slots(g, e, lo, hi);
+    units += (hi - lo + 255) / 256 * col_tiles;
+  }
+  for (int o = 32; o >= 1; o >>= 1) units += __shfl_xor(units, o);
+  units = __builtin_amdgcn_readfirstlane(units);
+  if (b >= units) return false;
+  const int xcd = b & 7, per = units >> 3, more = units & 7;
+  int index = xcd * per + min(xcd, more) + (b >> 3);
+  for (int e0 = 0; e0 < E; e0 += 64) {
+    const int e = e0 + lane;
+    int lo = 0, hi = 0;
+    if (e < E) expert_slots(g, e, lo, hi);
+    const int n = (hi - lo + 255) / 256;
+    int s = n * col_tiles;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int up = __shfl_up(s, o);
+      if (lane >= o) s += up;
+    }
+    const uint64_t past = __ballot(s > index);
+    if (past) {
+      const int at = __ffsll(static_cast<unsigned long long>(past)) - 1;
+      const int rows = __builtin_amdgcn_readlane(n, at);
+      index -= __builtin_amdgcn_readlane(s, at) - rows * col_tiles;
+      const int first = index / (4 * col_tiles) * 4, in = index - first * col_tiles, m = min(4, rows - first);
+      t.expert = e0 + at;
+      t.row0 = __builtin_amdgcn_readlane(lo, at) + static_cast<int64_t>(first + in % m) * 256;
+      t.end = __builtin_amdgcn_readlane(hi, at);
+      col = in / m;
+      return true;
+    }
+    index -= __builtin_amdgcn_readlane(s, 63);
   }
   return false;
 }
@@ -169,6 +211,221 @@ __global__ void __launch_bounds__(kWaves * 64) k_expert_stream(ExpertGemmArgs g,
   }
 }
 
+// ---------------------------------------------------------------------------
+// Many rows an expert: tiles of 256 slots by 256 columns, 4 waves of 64 columns each.
+//  - B needs no LDS: the image holds matrix operands, and a wave is the only reader of its 64 columns.  Its 8 loads of a
+//    128-deep stage (1 KB each) go to one of three register sets, two stages ahead.
+//  - A is read by all four waves: its rows move to a ring of four 32 KB stages in LDS (direct loads, 16-byte chunks of a
+//    row XOR-swizzled by row / 2 against bank conflicts), three stages ahead; one barrier a stage, halfway through,
+//    where every wave's part of the next stage has landed and the stage before this one has been read by all.
+//  - A wave's accumulators are 16 x 4 tiles of 16 x 16 (256 AGPRs, updated in place); each fragment of A is
+//    read two row tiles before its 4 MFMAs.
+//  - A tile of fewer slots runs the same loop over its blocks of 64 (NB = 1 .. 4).
+constexpr int kTM = 256, kTN = 256, kRing = 4, kSlot = kTM * 128;
+constexpr int kTileThreads = 256;
+
+// Waits until at most N of this wave's vector-memory operations are outstanding, then joins the workgroup's barrier; LDS
+// reads and younger loads keep flying.
+template <int N>
+__device__ __forceinline__ void stage_barrier() {
+  static_assert(N < 64, "vmcnt field");
+  __builtin_amdgcn_sched_barrier(0);
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_s_waitcnt(((N >> 4) << 14) | 0x0F70 | (N & 15));
+  __builtin_amdgcn_s_barrier();
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// Wait states between VALU accesses of 16 accumulators and inline MFMAs: 24, more than the 8-pass MFMA's distances.
+__device__ __forceinline__ void fence16(f32x4 (&a)[4][4]) {
+  asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7"
+               : "+a"(a[0][0]), "+a"(a[0][1]), "+a"(a[0][2]), "+a"(a[0][3]), "+a"(a[1][0]), "+a"(a[1][1]),
+                 "+a"(a[1][2]), "+a"(a[1][3]), "+a"(a[2][0]), "+a"(a[2][1]), "+a"(a[2][2]), "+a"(a[2][3]),
+                 "+a"(a[3][0]), "+a"(a[3][1]), "+a"(a[3][2]), "+a"(a[3][3]));
+}
+
+struct TileShared {
+  __attribute__((aligned(16))) uint8_t ring[kRing * kSlot];
+  int64_t row[kTM];  // the row of a of each slot, -1: none
+  float scale[kTM];
+};
+
+// The operands of one wave of a tile, fixed over its stages.
+struct TileOperands {
+  __amdgpu_buffer_rsrc_t a;
+  uint32_t voa[8];        // offsets of the rows that this lane loads
+  __amdgpu_buffer_rsrc_t b;
+  int goff[4];            // offsets of its groups of 16 columns
+  int lo, hi;             // offsets of the lane's two chunks of A in row tile 0 of a stage
+  int wave, lane, last;   // last: the last stage
+};
+
+__device__ __forceinline__ i32x8 load_b(const TileOperands& p, int j, int s) {
+  const int at = p.goff[j] + min(s, p.last) * 2048;
+  return join(__builtin_amdgcn_raw_buffer_load_b128(p.b, p.lane * 16, at, 0),
+              __builtin_amdgcn_raw_buffer_load_b128(p.b, p.lane * 16 + 1024, at, 0));
+}
+__device__ __forceinline__ void load_a(const TileOperands& p, TileShared& sh, int j, int s) {
+  dma1(p.a, min(s, p.last) * 128, p.voa[j], sh.ring + (s & (kRing - 1)) * kSlot, 4 * j + p.wave);
+}
+__device__ __forceinline__ i32x8 frag_a(const TileOperands& p, const TileShared& sh, int i, int s) {
+  const uint8_t* at = sh.ring + (s & (kRing - 1)) * kSlot + i * 2048;
+  return join(*reinterpret_cast<const u32x4*>(at + p.lo), *reinterpret_cast<const u32x4*>(at + p.hi));
+}
+
+// Stage s: B's fragments in bc.  kRound: the loads of stage s + 3 of A and s + 2 of B (to bn) are issued; kMore: all loads
+// have been, a stage may follow; kEnd: none does.  (The barrier's count is that of the loads issued after those of stage
+// s + 1 of A, which it waits for: a stage issues B's 8 before its barrier and A's 2 NB after it.)
+enum StageKind { kRound, kMore, kEnd };
+template <int FA, int NB, StageKind KIND>
+__device__ __forceinline__ void tile_stage(const TileOperands& p, TileShared& sh, int s, f32x4 (&acc)[NB][4][4],
+                                           i32x8 (&af)[4], const i32x8 (&bc)[4], i32x8 (&bn)[4]) {
+  constexpr int MI = 4 * NB;
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    if (i == MI / 2 && KIND != kEnd) stage_barrier<(KIND == kRound ? 16 : 8) + 2 * NB>();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      mfma16<FA>(acc[i / 4][i & 3][j], bc[j], af[i & 3]);
+      if (j == 0 && i + 2 < MI) af[(i + 2) & 3] = frag_a(p, sh, i + 2, s);
+      if (j == 0 && i + 2 >= MI && KIND != kEnd) af[(i + 2) & 3] = frag_a(p, sh, i + 2 - MI, s + 1);
+      if (KIND == kRound) {
+        if (i < 2 && (j & 1)) bn[2 * i + j / 2] = load_b(p, 2 * i + j / 2, s + 2);
+        const int d = 4 * (i - MI / 2) + j;
+        if (d >= 0 && d < 2 * NB) load_a(p, sh, d, s + 3);
+      }
+    }
+  }
+}
+
+template <int FA, int NB, typename O>
+__device__ __forceinline__ void tile_body(const ExpertGemmArgs& g, TileShared& sh, TileOperands& p, const Tile& t, int64_t n0) {
+  f32x4 acc[NB][4][4];
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[b][i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int b = 0; b < NB; ++b) fence16(acc[b]);
+  i32x8 b0[4], b1[4], b2[4], af[4];
+  auto stage_a = [&](int s) {
+#pragma unroll
+    for (int j = 0; j < 2 * NB; ++j) load_a(p, sh, j, s);
+  };
+  auto stage_b = [&](i32x8(&b)[4], int s) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) b[j] = load_b(p, j, s);
+  };
+  stage_a(0);
+  stage_b(b0, 0);
+  stage_a(1);
+  stage_b(b1, 1);
+  stage_a(2);
+  stage_barrier<16 + 4 * NB>();
+  af[0] = frag_a(p, sh, 0, 0);
+  af[1] = frag_a(p, sh, 1, 0);
+  // (whole rounds of the three register sets, then what is left: a loop with exits between them made the compiler wait
+  // for younger loads at its head)
+  const int ns = p.last + 1;
+  int s = 0;
+  for (; s + 3 <= ns; s += 3) {
+    tile_stage<FA, NB, kRound>(p, sh, s, acc, af, b0, b2);
+    tile_stage<FA, NB, kRound>(p, sh, s + 1, acc, af, b1, b0);
+    tile_stage<FA, NB, kRound>(p, sh, s + 2, acc, af, b2, b1);
+  }
+  if (s < ns) tile_stage<FA, NB, kMore>(p, sh, s, acc, af, b0, b2);
+  if (s + 1 < ns) tile_stage<FA, NB, kEnd>(p, sh, s + 1, acc, af, b1, b0);
+#pragma unroll
+  for (int b = 0; b < NB; ++b) fence16(acc[b]);
+  step_barrier<0>();  // every load has landed and every fragment is read: the ring is free
+
+  // Lane: slots 16 i + fr, columns 16 j + 4 q .. of the wave's 64.  Rows go through the wave's 32 KB of the ring
+  // (16-byte chunks XOR-swizzled by row) to stores of whole 16-byte chunks.
+  const int fr = p.lane & 15, q = p.lane >> 4;
+  const int64_t col0 = n0 + 64 * p.wave;
+  float sb[4][4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      sb[j][e] = g.sb[t.expert * g.sb_expert + min(col0 + 16 * j + 4 * q + e, g.N - 1) * g.sb_col];
+  constexpr int kRowBytes = 64 * sizeof(O), kChunks = kRowBytes / 16;
+  constexpr int kRows = 64 * NB < kSlot / kRowBytes ? 64 * NB : kSlot / kRowBytes;  // rows of one pass
+  uint8_t* mine = sh.ring + p.wave * kSlot;
+#pragma unroll
+  for (int r0 = 0; r0 < 64 * NB; r0 += kRows) {
+#pragma unroll
+    for (int i = r0 / 16; i < (r0 + kRows) / 16; ++i) {
+      const int r = 16 * i + fr;
+      const float sa = sh.scale[r];
+      const bool none = sh.row[r] < 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        f32x4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = none ? 0.0f : acc[i / 4][i & 3][j][e] * (sa * sb[j][e]);
+        const int byte = (16 * j + 4 * q) * static_cast<int>(sizeof(O));
+        uint8_t* dst = mine + (r - r0) * kRowBytes + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15);
+        store4(reinterpret_cast<O*>(dst), v);
+      }
+    }
+    for (int c = p.lane; c < kRows * kChunks; c += 64) {
+      const int r = c / kChunks, k = c % kChunks;
+      const int64_t s = t.row0 + r0 + r, col = col0 + k * (16 / static_cast<int>(sizeof(O)));
+      const u32x4 v = *reinterpret_cast<const u32x4*>(mine + r * kRowBytes + ((k ^ (r & 7)) << 4));
+      if (s < t.end && col < g.N) *reinterpret_cast<u32x4*>(static_cast<O*>(g.y) + s * g.ldy + col) = v;
+    }
+  }
+}
+
+template <int FA, typename O>
+__global__ void __launch_bounds__(kTileThreads, 1) k_expert_tile(ExpertGemmArgs g, FastDiv choices, int col_tiles) {
+  __shared__ TileShared sh;
+  Tile t;
+  int col;
+  if (!find_unit(g, blockIdx.x, col_tiles, t, col)) return;
+  const int tid = threadIdx.x;
+  TileOperands p;
+  p.lane = tid & 63;
+  p.wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  {
+    const int64_t s = min(t.row0 + tid, t.end - 1);
+    const int64_t row = row_of(g, choices, s);
+    sh.row[tid] = row;
+    sh.scale[tid] = g.sa[g.sa_rows ? max(row, int64_t(0)) : 0];
+  }
+  __syncthreads();
+  const int nb = static_cast<int>((min(t.end - t.row0, int64_t(kTM)) + 63) / 64);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int r = (4 * j + p.wave) * 8 + (p.lane >> 3);
+    const int c = (p.lane & 7) ^ ((r >> 1) & 7);
+    p.voa[j] = static_cast<uint32_t>(max(sh.row[r], int64_t(0)) * g.lda + c * 16);
+  }
+  p.a = __builtin_amdgcn_make_buffer_rsrc(uniform_ptr(g.a), 0, -1, 0x00020000);
+  const int groups = static_cast<int>(g.N / 16);
+  const int64_t steps = g.K / 128;
+  p.last = static_cast<int>(steps) - 1;
+  const int g0 = min(col * (kTN / 16) + p.wave * 4, groups - 1);  // (waves past the last column repeat it)
+  p.b = __builtin_amdgcn_make_buffer_rsrc(
+      uniform_ptr(g.b + (static_cast<int64_t>(t.expert) * groups + g0) * steps * 2048), 0, -1, 0x00020000);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) p.goff[j] = __builtin_amdgcn_readfirstlane(static_cast<int>(min(j, groups - 1 - g0) * steps * 2048));
+  const int fr = p.lane & 15, q = p.lane >> 4, sw = (fr >> 1) & 7;
+  p.lo = fr * 128 + (((2 * q) ^ sw) << 4);
+  p.hi = fr * 128 + (((2 * q + 1) ^ sw) << 4);
+  const int64_t n0 = static_cast<int64_t>(col) * kTN;
+  switch (nb) {
+    case 1: tile_body<FA, 1, O>(g, sh, p, t, n0); break;
+    case 2: tile_body<FA, 2, O>(g, sh, p, t, n0); break;
+    case 3: tile_body<FA, 3, O>(g, sh, p, t, n0); break;
+    default: tile_body<FA, 4, O>(g, sh, p, t, n0); break;
+  }
+}
+
 }  // namespace
 
 hipError_t launch_expert_gemm(const ExpertGemmArgs& g, hipStream_t st) {
@@ -185,7 +442,20 @@ hipError_t launch_expert_gemm(const ExpertGemmArgs& g, hipStream_t st) {
     hipLaunchKernelGGL((k_expert_stream<FA, O, MT, NT>), dim3(static_cast<unsigned>(tiles * chunks)), dim3(kWaves * 64), 0,
                        st, g, choices, static_cast<int>(chunks), ks);
   };
+  auto tile = [&](auto fa, auto o) {
+    constexpr int FA = decltype(fa)::value;
+    using O = decltype(o);
+    const int64_t col_tiles = ceil_div(g.N, kTN), rows = g.slots / kTM + std::min(g.experts, g.slots);
+    hipLaunchKernelGGL((k_expert_tile<FA, O>), dim3(static_cast<unsigned>(rows * col_tiles)), dim3(kTileThreads), 0, st, g,
+                       choices, static_cast<int>(col_tiles));
+  };
+  static const int force = getenv("FP8RT_EXP") ? atoi(getenv("FP8RT_EXP")) : -1;
   auto by_rows = [&](auto fa, auto o) {
+    if (force == 9 || (force < 0 && avg > 32)) return tile(fa, o);
+    if (force == 0) return stream(fa, o, std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
+    if (force == 1) return stream(fa, o, std::integral_constant<int, 1>{}, std::integral_constant<int, 2>{});
+    if (force == 2) return stream(fa, o, std::integral_constant<int, 2>{}, std::integral_constant<int, 2>{});
+    if (force == 4) return stream(fa, o, std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
     if (avg <= 16) stream(fa, o, std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
     else if (avg <= 32) stream(fa, o, std::integral_constant<int, 2>{}, std::integral_constant<int, 2>{});
     else stream(fa, o, std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
