@@ -2,8 +2,6 @@
 // router's plan, against each expert's FP8 weights (one fragment-ordered image).
 //
 //   y[s,n] = s_a(r) s_b(e,n) sum_k dec(a[r,k]) dec(b[e,n,k]),   offsets[e] <= s < offsets[e+1]
-#include <stdlib.h>
-
 #include <algorithm>
 
 #include "gemm_tile.h"
@@ -57,17 +55,21 @@ __device__ __forceinline__ bool find_tile(const ExpertGemmArgs& g, int index, Ti
   return false;
 }
 
-// Work unit of workgroup b of the tile kernel: (row tile, column tile).  Experts one after the other; inside an expert
-// groups of 4 row tiles go through the column tiles together; each XCD (workgroups are dealt to the 8 in turn) gets a
-// contiguous range of that order, so that its L2 serves what neighbours share.  False past the last.
+// Work unit of workgroup b of the tile kernel: (row tile of TM slots, column tile).  Experts one after the other; inside an
+// expert groups of 4 row tiles go through the column tiles together; each XCD (workgroups are dealt to the 8 in turn)
+// gets a contiguous range of that order, so that its L2 serves what neighbours share.  False past the last.
+template <int TM>
 __device__ __forceinline__ bool find_unit(const ExpertGemmArgs& g, int b, int col_tiles, Tile& t, int& col) {
   const int lane = threadIdx.x & 63, E = static_cast<int>(g.experts);
-  int units = 0;
-  for (int e = lane; e < E; e += 64) {
+  int lo0 = 0, hi0 = 0;  // the first 64 experts' slots are kept for the second pass
+  if (lane < E) expert_slots(g, lane, lo0, hi0);
+  int units = (hi0 - lo0 + TM - 1) / TM * col_tiles;
+  for (int e = 64 + lane; e < E; e += 64) {
     int lo, hi;
     expert_slots(g, e, lo, hi);
-    units += (hi - lo + 255) / 256 * col_tiles;
+    units += (hi - lo + TM - 1) / TM * col_tiles;
   }
+#pragma unroll
   for (int o = 32; o >= 1; o >>= 1) units += __shfl_xor(units, o);
   units = __builtin_amdgcn_readfirstlane(units);
   if (b >= units) return false;
@@ -75,9 +77,12 @@ __device__ __forceinline__ bool find_unit(const ExpertGemmArgs& g, int b, int co
   int index = xcd * per + min(xcd, more) + (b >> 3);
   for (int e0 = 0; e0 < E; e0 += 64) {
     const int e = e0 + lane;
-    int lo = 0, hi = 0;
-    if (e < E) expert_slots(g, e, lo, hi);
-    const int n = (hi - lo + 255) / 256;
+    int lo = lo0, hi = hi0;
+    if (e0 > 0) {
+      lo = hi = 0;
+      if (e < E) expert_slots(g, e, lo, hi);
+    }
+    const int n = (hi - lo + TM - 1) / TM;
     int s = n * col_tiles;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
@@ -91,7 +96,7 @@ __device__ __forceinline__ bool find_unit(const ExpertGemmArgs& g, int b, int co
       index -= __builtin_amdgcn_readlane(s, at) - rows * col_tiles;
       const int first = index / (4 * col_tiles) * 4, in = index - first * col_tiles, m = min(4, rows - first);
       t.expert = e0 + at;
-      t.row0 = __builtin_amdgcn_readlane(lo, at) + static_cast<int64_t>(first + in % m) * 256;
+      t.row0 = __builtin_amdgcn_readlane(lo, at) + static_cast<int64_t>(first + in % m) * TM;
       t.end = __builtin_amdgcn_readlane(hi, at);
       col = in / m;
       return true;
@@ -221,7 +226,7 @@ __global__ void __launch_bounds__(kWaves * 64) k_expert_stream(ExpertGemmArgs g,
 //  - A wave's accumulators are 16 x 4 tiles of 16 x 16 (256 AGPRs, updated in place); each fragment of A is
 //    read two row tiles before its 4 MFMAs.
 //  - A tile of fewer slots runs the same loop over its blocks of 64 (NB = 1 .. 4).
-constexpr int kTM = 256, kTN = 256, kRing = 4, kSlot = kTM * 128;
+constexpr int kTN = 256, kRing = 4;
 constexpr int kTileThreads = 256;
 
 // Waits until at most N of this wave's vector-memory operations are outstanding, then joins the workgroup's barrier; LDS
@@ -245,10 +250,12 @@ __device__ __forceinline__ void fence16(f32x4 (&a)[4][4]) {
                  "+a"(a[3][0]), "+a"(a[3][1]), "+a"(a[3][2]), "+a"(a[3][3]));
 }
 
-struct TileShared {
+template <int BLOCKS>
+struct TileShared {  // for tiles of up to BLOCKS blocks of 64 slots
+  static constexpr int kSlot = BLOCKS * 64 * 128;
   __attribute__((aligned(16))) uint8_t ring[kRing * kSlot];
-  int64_t row[kTM];  // the row of a of each slot, -1: none
-  float scale[kTM];
+  int row[64 * BLOCKS];  // the row of a of each slot, -1: none
+  float scale[64 * BLOCKS];
 };
 
 // The operands of one wave of a tile, fixed over its stages.
@@ -266,11 +273,13 @@ __device__ __forceinline__ i32x8 load_b(const TileOperands& p, int j, int s) {
   return join(__builtin_amdgcn_raw_buffer_load_b128(p.b, p.lane * 16, at, 0),
               __builtin_amdgcn_raw_buffer_load_b128(p.b, p.lane * 16 + 1024, at, 0));
 }
-__device__ __forceinline__ void load_a(const TileOperands& p, TileShared& sh, int j, int s) {
-  dma1(p.a, min(s, p.last) * 128, p.voa[j], sh.ring + (s & (kRing - 1)) * kSlot, 4 * j + p.wave);
+template <int BLOCKS>
+__device__ __forceinline__ void load_a(const TileOperands& p, TileShared<BLOCKS>& sh, int j, int s) {
+  dma1(p.a, min(s, p.last) * 128, p.voa[j], sh.ring + (s & (kRing - 1)) * sh.kSlot, 4 * j + p.wave);
 }
-__device__ __forceinline__ i32x8 frag_a(const TileOperands& p, const TileShared& sh, int i, int s) {
-  const uint8_t* at = sh.ring + (s & (kRing - 1)) * kSlot + i * 2048;
+template <int BLOCKS>
+__device__ __forceinline__ i32x8 frag_a(const TileOperands& p, const TileShared<BLOCKS>& sh, int i, int s) {
+  const uint8_t* at = sh.ring + (s & (kRing - 1)) * sh.kSlot + i * 2048;
   return join(*reinterpret_cast<const u32x4*>(at + p.lo), *reinterpret_cast<const u32x4*>(at + p.hi));
 }
 
@@ -278,8 +287,8 @@ __device__ __forceinline__ i32x8 frag_a(const TileOperands& p, const TileShared&
 // have been, a stage may follow; kEnd: none does.  (The barrier's count is that of the loads issued after those of stage
 // s + 1 of A, which it waits for: a stage issues B's 8 before its barrier and A's 2 NB after it.)
 enum StageKind { kRound, kMore, kEnd };
-template <int FA, int NB, StageKind KIND>
-__device__ __forceinline__ void tile_stage(const TileOperands& p, TileShared& sh, int s, f32x4 (&acc)[NB][4][4],
+template <int FA, int NB, StageKind KIND, int BLOCKS>
+__device__ __forceinline__ void tile_stage(const TileOperands& p, TileShared<BLOCKS>& sh, int s, f32x4 (&acc)[NB][4][4],
                                            i32x8 (&af)[4], const i32x8 (&bc)[4], i32x8 (&bn)[4]) {
   constexpr int MI = 4 * NB;
 #pragma unroll
@@ -299,8 +308,9 @@ __device__ __forceinline__ void tile_stage(const TileOperands& p, TileShared& sh
   }
 }
 
-template <int FA, int NB, typename O>
-__device__ __forceinline__ void tile_body(const ExpertGemmArgs& g, TileShared& sh, TileOperands& p, const Tile& t, int64_t n0) {
+template <int FA, int NB, typename O, int BLOCKS>
+__device__ __forceinline__ void tile_body(const ExpertGemmArgs& g, TileShared<BLOCKS>& sh, TileOperands& p, const Tile& t,
+                                          int64_t n0, i32x8 (&b0)[4], i32x8 (&b1)[4]) {
   f32x4 acc[NB][4][4];
 #pragma unroll
   for (int b = 0; b < NB; ++b)
@@ -310,24 +320,15 @@ __device__ __forceinline__ void tile_body(const ExpertGemmArgs& g, TileShared& s
       for (int j = 0; j < 4; ++j) acc[b][i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int b = 0; b < NB; ++b) fence16(acc[b]);
-  i32x8 b0[4], b1[4], b2[4], af[4];
-  auto stage_a = [&](int s) {
+  i32x8 b2[4], af[4];
+#pragma unroll
+  for (int s = 0; s < 3; ++s)
 #pragma unroll
     for (int j = 0; j < 2 * NB; ++j) load_a(p, sh, j, s);
-  };
-  auto stage_b = [&](i32x8(&b)[4], int s) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) b[j] = load_b(p, j, s);
-  };
-  stage_a(0);
-  stage_b(b0, 0);
-  stage_a(1);
-  stage_b(b1, 1);
-  stage_a(2);
-  stage_barrier<16 + 4 * NB>();
+  stage_barrier<2 * NB>();  // stages 0 and 1 of A have landed
   af[0] = frag_a(p, sh, 0, 0);
   af[1] = frag_a(p, sh, 1, 0);
-  // (whole rounds of the three register sets, then what is left: a loop with exits between them made the compiler wait
+  // (whole rounds of the register sets, then what is left: a loop with exits between them made the compiler wait
   // for younger loads at its head)
   const int ns = p.last + 1;
   int s = 0;
@@ -342,7 +343,7 @@ __device__ __forceinline__ void tile_body(const ExpertGemmArgs& g, TileShared& s
   for (int b = 0; b < NB; ++b) fence16(acc[b]);
   step_barrier<0>();  // every load has landed and every fragment is read: the ring is free
 
-  // Lane: slots 16 i + fr, columns 16 j + 4 q .. of the wave's 64.  Rows go through the wave's 32 KB of the ring
+  // Lane: slots 16 i + fr, columns 16 j + 4 q .. of the wave's 64.  Rows go through the wave's quarter of the ring
   // (16-byte chunks XOR-swizzled by row) to stores of whole 16-byte chunks.
   const int fr = p.lane & 15, q = p.lane >> 4;
   const int64_t col0 = n0 + 64 * p.wave;
@@ -353,6 +354,7 @@ __device__ __forceinline__ void tile_body(const ExpertGemmArgs& g, TileShared& s
     for (int e = 0; e < 4; ++e)
       sb[j][e] = g.sb[t.expert * g.sb_expert + min(col0 + 16 * j + 4 * q + e, g.N - 1) * g.sb_col];
   constexpr int kRowBytes = 64 * sizeof(O), kChunks = kRowBytes / 16;
+  constexpr int kSlot = TileShared<BLOCKS>::kSlot;
   constexpr int kRows = 64 * NB < kSlot / kRowBytes ? 64 * NB : kSlot / kRowBytes;  // rows of one pass
   uint8_t* mine = sh.ring + p.wave * kSlot;
 #pragma unroll
@@ -381,31 +383,29 @@ __device__ __forceinline__ void tile_body(const ExpertGemmArgs& g, TileShared& s
   }
 }
 
-template <int FA, typename O>
-__global__ void __launch_bounds__(kTileThreads, 1) k_expert_tile(ExpertGemmArgs g, FastDiv choices, int col_tiles) {
-  __shared__ TileShared sh;
+// Joins the workgroup's barrier with the wave's LDS operations done; loads keep flying.
+__device__ __forceinline__ void lds_join() {
+  __builtin_amdgcn_sched_barrier(0);
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// Tiles of up to BLOCKS blocks of 64 slots.  Four blocks take most of the registers and the LDS (one workgroup a CU); with
+// one block a second workgroup fills the first one's start, end and barriers.
+template <int FA, typename O, int BLOCKS>
+__global__ void __launch_bounds__(kTileThreads, BLOCKS == 4 ? 1 : 2) k_expert_tile(ExpertGemmArgs g, FastDiv choices, int col_tiles) {
+  __shared__ TileShared<BLOCKS> sh;
+  constexpr int TM = 64 * BLOCKS;
   Tile t;
   int col;
-  if (!find_unit(g, blockIdx.x, col_tiles, t, col)) return;
+  if (!find_unit<TM>(g, blockIdx.x, col_tiles, t, col)) return;
   const int tid = threadIdx.x;
   TileOperands p;
   p.lane = tid & 63;
   p.wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  {
-    const int64_t s = min(t.row0 + tid, t.end - 1);
-    const int64_t row = row_of(g, choices, s);
-    sh.row[tid] = row;
-    sh.scale[tid] = g.sa[g.sa_rows ? max(row, int64_t(0)) : 0];
-  }
-  __syncthreads();
-  const int nb = static_cast<int>((min(t.end - t.row0, int64_t(kTM)) + 63) / 64);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int r = (4 * j + p.wave) * 8 + (p.lane >> 3);
-    const int c = (p.lane & 7) ^ ((r >> 1) & 7);
-    p.voa[j] = static_cast<uint32_t>(max(sh.row[r], int64_t(0)) * g.lda + c * 16);
-  }
-  p.a = __builtin_amdgcn_make_buffer_rsrc(uniform_ptr(g.a), 0, -1, 0x00020000);
   const int groups = static_cast<int>(g.N / 16);
   const int64_t steps = g.K / 128;
   p.last = static_cast<int>(steps) - 1;
@@ -414,51 +414,82 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_expert_tile(ExpertGemmArgs 
       uniform_ptr(g.b + (static_cast<int64_t>(t.expert) * groups + g0) * steps * 2048), 0, -1, 0x00020000);
 #pragma unroll
   for (int j = 0; j < 4; ++j) p.goff[j] = __builtin_amdgcn_readfirstlane(static_cast<int>(min(j, groups - 1 - g0) * steps * 2048));
+  i32x8 b0[4], b1[4];  // the first loads of B fly while the rows of a are looked up
+#pragma unroll
+  for (int j = 0; j < 4; ++j) b0[j] = load_b(p, j, 0);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) b1[j] = load_b(p, j, 1);
+  if (tid < TM) {
+    const int64_t row = row_of(g, choices, min(t.row0 + tid, t.end - 1));
+    sh.row[tid] = static_cast<int>(row);
+    sh.scale[tid] = g.sa[g.sa_rows ? max(row, int64_t(0)) : 0];
+  }
+  lds_join();
+  const int nb = static_cast<int>((min(t.end - t.row0, int64_t(TM)) + 63) / 64);
+#pragma unroll
+  for (int j = 0; j < 2 * BLOCKS; ++j) {
+    const int r = (4 * j + p.wave) * 8 + (p.lane >> 3);
+    const int c = (p.lane & 7) ^ ((r >> 1) & 7);
+    p.voa[j] = static_cast<uint32_t>(static_cast<int64_t>(max(sh.row[r], 0)) * g.lda + c * 16);
+  }
+  p.a = __builtin_amdgcn_make_buffer_rsrc(uniform_ptr(g.a), 0, -1, 0x00020000);
   const int fr = p.lane & 15, q = p.lane >> 4, sw = (fr >> 1) & 7;
   p.lo = fr * 128 + (((2 * q) ^ sw) << 4);
   p.hi = fr * 128 + (((2 * q + 1) ^ sw) << 4);
   const int64_t n0 = static_cast<int64_t>(col) * kTN;
-  switch (nb) {
-    case 1: tile_body<FA, 1, O>(g, sh, p, t, n0); break;
-    case 2: tile_body<FA, 2, O>(g, sh, p, t, n0); break;
-    case 3: tile_body<FA, 3, O>(g, sh, p, t, n0); break;
-    default: tile_body<FA, 4, O>(g, sh, p, t, n0); break;
+  if constexpr (BLOCKS == 1) {
+    tile_body<FA, 1, O>(g, sh, p, t, n0, b0, b1);
+  } else {
+    switch (nb) {
+      case 1: tile_body<FA, 1, O>(g, sh, p, t, n0, b0, b1); break;
+      case 2: tile_body<FA, 2, O>(g, sh, p, t, n0, b0, b1); break;
+      case 3: tile_body<FA, 3, O>(g, sh, p, t, n0, b0, b1); break;
+      default: tile_body<FA, 4, O>(g, sh, p, t, n0, b0, b1); break;
+    }
   }
 }
 
 }  // namespace
 
+// Which kernel.  The host knows the slots and the experts, not how the plan shares them out, so the rule goes by the
+// average a = slots / experts and by the units that the tile kernel would have at most.  Measured with equal
+// experts, N x K, us (stream of 16 / of 32 slots, tiles of 64 / of 256; the weights alone at 6.1 TB/s):
+//   4096 x 7168,  32 experts of  4 slots: 139 / 144, 160 / 160 (154)      of 16: 169 / 153, 162 / 162
+//   7168 x 2048,  32 experts of  8 slots:  88 /  98,  87 /  92  (77)      of 32: 170 / 110,  92 /  98
+//   4096 x 7168,   8 experts of 16 slots:  44 /  44,  62 /  53  (38)      of 32:  67 /  54,  64 /  55  (128 units)
+//   4096 x 7168,   2 experts of 16 slots:  14 /  16,  37 /  27  (10)      of 32:  25 /  17,  37 /  28   (32 units)
+//   4096 x 7168,  32 experts of 64 slots: tiles of 64 / of 256 169 / 171, of 128: 221 / 190
+//   2048 x 2048, 128 experts of 64 slots: 106 / 113, of 128: 142 / 138;  8 experts of 64, 4096 x 7168 (128 units): 67 / 59
+// A few slots an expert are streamed; from 9 on tiles win where they fill the CUs, from 33 on always.  Tiles of
+// 64 (two workgroups a CU) up to 64 slots where there are units for both.
 hipError_t launch_expert_gemm(const ExpertGemmArgs& g, hipStream_t st) {
   const FastDiv choices(static_cast<uint32_t>(g.choices));
-  const int64_t avg = g.slots / g.experts;
+  const int64_t a = ceil_div(g.slots, g.experts), col_tiles = ceil_div(g.N, kTN), cus = device_cus();
   auto stream = [&](auto fa, auto o, auto mt, auto nt) {
     constexpr int FA = decltype(fa)::value, MT = decltype(mt)::value, NT = decltype(nt)::value;
     using O = decltype(o);
     const int64_t tiles = g.slots / (16 * MT) + std::min(g.experts, g.slots);
     const int64_t sets = ceil_div(g.N / 16, NT);
-    int ks = 1;  // waves for each set of columns: 8 waves a CU at least, if the steps allow it
-    while (ks < kWaves && tiles * sets * ks < int64_t(device_cus()) * 16 && g.K / 128 >= 4 * ks) ks <<= 1;
+    int ks = 1;  // waves for each set of columns: 16 waves a CU, if the steps allow it
+    while (ks < kWaves && tiles * sets * ks < cus * 16 && g.K / 128 >= 4 * ks) ks <<= 1;
     const int64_t chunks = ceil_div(sets, kWaves / ks);
     hipLaunchKernelGGL((k_expert_stream<FA, O, MT, NT>), dim3(static_cast<unsigned>(tiles * chunks)), dim3(kWaves * 64), 0,
                        st, g, choices, static_cast<int>(chunks), ks);
   };
-  auto tile = [&](auto fa, auto o) {
-    constexpr int FA = decltype(fa)::value;
+  auto tile = [&](auto fa, auto o, auto blocks) {
+    constexpr int FA = decltype(fa)::value, BLOCKS = decltype(blocks)::value;
     using O = decltype(o);
-    const int64_t col_tiles = ceil_div(g.N, kTN), rows = g.slots / kTM + std::min(g.experts, g.slots);
-    hipLaunchKernelGGL((k_expert_tile<FA, O>), dim3(static_cast<unsigned>(rows * col_tiles)), dim3(kTileThreads), 0, st, g,
-                       choices, static_cast<int>(col_tiles));
+    const int64_t rows = g.slots / (64 * BLOCKS) + std::min(g.experts, g.slots);
+    hipLaunchKernelGGL((k_expert_tile<FA, O, BLOCKS>), dim3(static_cast<unsigned>(rows * col_tiles)), dim3(kTileThreads), 0,
+                       st, g, choices, static_cast<int>(col_tiles));
   };
-  static const int force = getenv("FP8RT_EXP") ? atoi(getenv("FP8RT_EXP")) : -1;
   auto by_rows = [&](auto fa, auto o) {
-    if (force == 9 || (force < 0 && avg > 32)) return tile(fa, o);
-    if (force == 0) return stream(fa, o, std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
-    if (force == 1) return stream(fa, o, std::integral_constant<int, 1>{}, std::integral_constant<int, 2>{});
-    if (force == 2) return stream(fa, o, std::integral_constant<int, 2>{}, std::integral_constant<int, 2>{});
-    if (force == 4) return stream(fa, o, std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
-    if (avg <= 16) stream(fa, o, std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
-    else if (avg <= 32) stream(fa, o, std::integral_constant<int, 2>{}, std::integral_constant<int, 2>{});
-    else stream(fa, o, std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
+    using std::integral_constant;
+    const int64_t units = std::min(g.experts, g.slots) * col_tiles;
+    if (a <= 8 || (a <= 16 && units < cus)) return stream(fa, o, integral_constant<int, 1>{}, integral_constant<int, 1>{});
+    if (a <= 32 && units < cus) return stream(fa, o, integral_constant<int, 2>{}, integral_constant<int, 2>{});
+    if (a <= 64 && units >= 2 * cus) return tile(fa, o, integral_constant<int, 1>{});
+    tile(fa, o, integral_constant<int, 4>{});
   };
   auto by_out = [&](auto fa) { g.yt == FP8RT_BF16 ? by_rows(fa, uint16_t{}) : by_rows(fa, float{}); };
   g.fa == FP8RT_E4M3 ? by_out(std::integral_constant<int, kE4M3>{}) : by_out(std::integral_constant<int, kE5M2>{});
