@@ -43,7 +43,7 @@ __device__ __forceinline__ void combine8(const CombineArgs& a, int64_t t, int64_
   store8(static_cast<T*>(a.y) + t * a.ldy + c, y);
 }
 template <typename T>
-__global__ void __launch_bounds__(256) k_combine(CombineArgs a, int64_t chunks) {
+__global__ void __launch_bounds__(64) k_combine(CombineArgs a, int64_t chunks) {
   for (int64_t i = blockIdx.x; i < a.tokens * chunks; i += gridDim.x) {
     const int64_t t = i / chunks, c = ((i - t * chunks) * blockDim.x + threadIdx.x) * 8;
     if (c < a.cols) combine8<T>(a, t, c);
@@ -65,19 +65,28 @@ __global__ void __launch_bounds__(1024) k_combine_backward(CombineArgs a) {
       Octet<T> g;
       g.load_nt(dy + c);
 #pragma unroll
-      for (int j = 0; j < K; ++j) {
-        const int64_t s = j < a.k ? slots[j] : -1;
-        if (s < 0 || s >= a.x_rows) continue;
-        Octet<T> o;
-        o.load_nt(x + s * a.ldx + c);
-        const float wj = w[j];
-        float d[8];
+      for (int j0 = 0; j0 < K; j0 += 8) {
+        if (j0 >= a.k) break;
+        Octet<T> o[8];  // (all loads before the stores, which they might otherwise have to wait for: dx may be x)
+        int64_t s[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          dot[j] += g.get(i) * o.get(i);
-          d[i] = wj * g.get(i);
+        for (int j = 0; j < 8; ++j) {
+          s[j] = j0 + j < a.k ? slots[j0 + j] : -1;
+          if (s[j] >= a.x_rows) s[j] = -1;
+          if (s[j] >= 0) o[j].load_nt(x + s[j] * a.ldx + c);
         }
-        store8(dx + s * a.lddx + c, d);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (s[j] < 0) continue;
+          const float wj = w[j0 + j];
+          float d[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            dot[j0 + j] += g.get(i) * o[j].get(i);
+            d[i] = wj * g.get(i);
+          }
+          store8(dx + s[j] * a.lddx + c, d);
+        }
       }
     }
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nw = blockDim.x >> 6;
@@ -100,7 +109,7 @@ __global__ void __launch_bounds__(1024) k_combine_backward(CombineArgs a) {
 
 hipError_t launch_expert_combine(const CombineArgs& a, hipStream_t st) {
   const int64_t octets = a.cols >> 3;
-  const int threads = octets >= 256 ? 256 : static_cast<int>(ceil_div(octets, 64) * 64);
+  const int threads = 64;  // (workgroups of one wave: 120 us where 128 / 256 / 512 threads took 122 / 130 / 127)
   const int64_t chunks = ceil_div(octets, threads);
   const dim3 grid(static_cast<unsigned>(std::min(a.tokens * chunks, kMaxGrid)));
   if (a.xt == FP8RT_BF16)
@@ -112,7 +121,10 @@ hipError_t launch_expert_combine(const CombineArgs& a, hipStream_t st) {
 
 hipError_t launch_expert_combine_backward(const CombineArgs& a, hipStream_t st) {
   const int64_t octets = a.cols >> 3;
-  const int threads = octets >= 1024 ? 1024 : static_cast<int>(ceil_div(octets, 64) * 64);
+  // many tokens: a quarter of 1024 threads each, so that several workgroups a CU overlap loads and sums (4096 tokens of
+  // 7168: 204 us, 64 / 128 / 1024 threads 207 / 222 / 211); few: one round of columns (64 tokens: 11 us against 20)
+  const int64_t most = a.tokens >= 2 * device_cus() ? 256 : 1024;
+  const int threads = static_cast<int>(ceil_div(ceil_div(octets, ceil_div(octets, most)), 64) * 64);
   const dim3 grid(static_cast<unsigned>(std::min(a.tokens, kMaxGrid)));
   auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, dim3(threads), 0, st, a); };
   auto by_k = [&](auto t) {

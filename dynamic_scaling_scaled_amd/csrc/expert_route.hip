@@ -2,8 +2,10 @@
 // k largest, weights, the plan that sorts the choices by expert; and the weights' gradient.
 //
 // A wave takes a token: lane l holds experts l NV .. l NV + NV - 1, so the lowest lane of a tie holds the lowest
-// expert.  Keys are compared as integers that rise with them: the logit itself without a bias (softmax and sigmoid rise with
-// it, so nothing is computed to choose), binary64 scores with one.
+// expert.  Keys are compared as integers that rise with them.  Without a bias the logit itself is the key (softmax and
+// sigmoid rise with it, so nothing is computed to choose); scores with a bias, and groups' sums of scores, are
+// formed in binary32 first, with a bound of their error, and in binary64 for the tokens where that bound leaves the
+// choice open.
 // The plan: a token chooses an expert at most once, so the tokens of one workgroup that chose expert e are
 // a 64-bit mask; a choice's place among its expert's is the number of set bits below its token (stable and free of
 // atomics on counters), and a workgroup's count is the mask's population.
@@ -54,11 +56,23 @@ __device__ __forceinline__ float wave_max(float v) {  // (finite, or -Inf)
   const uint32_t m = wave_max((b & 0x80000000u) ? ~b : b | 0x80000000u);
   return __uint_as_float((m & 0x80000000u) ? m & 0x7FFFFFFFu : ~m);
 }
-template <typename V>
-__device__ __forceinline__ V wave_sum(V v) {
+__device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
   return v;
+}
+// In binary32 by row shifts, as the maximum: 6 additions in a fixed order.
+__device__ __forceinline__ float wave_sum(float v) {
+#define FP8RT_DPP_ADD(CTRL, ROWS) \
+  v += __uint_as_float(__builtin_amdgcn_update_dpp(0, static_cast<int>(__float_as_uint(v)), CTRL, ROWS, 0xF, false))
+  FP8RT_DPP_ADD(0x111, 0xF);
+  FP8RT_DPP_ADD(0x112, 0xF);
+  FP8RT_DPP_ADD(0x114, 0xF);
+  FP8RT_DPP_ADD(0x118, 0xF);
+  FP8RT_DPP_ADD(0x142, 0xA);
+  FP8RT_DPP_ADD(0x143, 0xC);
+#undef FP8RT_DPP_ADD
+  return __uint_as_float(__builtin_amdgcn_readlane(static_cast<int>(__float_as_uint(v)), 63));
 }
 
 // The lane of the largest key, the lowest of a tie (its key is returned; 0: no lane has one).  `low`: the
@@ -122,14 +136,250 @@ __device__ __forceinline__ uint32_t exclusive_sum(uint32_t& v, uint32_t* part) {
 }
 
 // ---------------------------------------------------------------------------
-// Forward.  Workgroup b takes tokens b plan.tokens ..; with one workgroup the plan is finished here.
+// Forward.
+
+// Keys as 32 bits: a binary32 value's.
+__device__ __forceinline__ uint32_t rising32(float v) { return static_cast<uint32_t>(rising(v) >> 32); }
+__device__ __forceinline__ float number32(uint32_t r) {
+  return __uint_as_float((r & 0x80000000u) ? r & 0x7FFFFFFFu : ~r);
+}
+
+// The groups of a call: runs of n experts.
+struct Groups {
+  int n;              // experts of a group
+  int lanes;          // lanes that hold one (n / NV, where that is a power of two), or 0
+  FastDiv by_n;
+};
+
+// The two largest keys of every group, in all of its lanes: `lanes` lanes that hold its experts, or P lanes that read
+// its members from `mine` (LDS of this wave).  Lane l belongs to group l / per (returned).
+template <typename K, int NV>
+__device__ __forceinline__ int group_tops(const RouteArgs& a, const Groups& gr, const K (&key)[NV], K* mine, K& b1, K& b2) {
+  const int lane = threadIdx.x & 63;
+  b1 = b2 = 0;
+  int per = gr.lanes;
+  if (per) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      b2 = max(b2, min(b1, key[v]));
+      b1 = max(b1, key[v]);
+    }
+  } else {
+    int gp = 1;
+    while (gp < a.groups) gp <<= 1;
+    per = 64 / gp;
+    const int g = lane / per;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+      if (lane * NV + v < a.experts) mine[lane * NV + v] = key[v];
+    __builtin_amdgcn_wave_barrier();
+    if (g < a.groups) {
+      for (int i = lane - g * per; i < gr.n; i += per) {
+        const K x = mine[g * gr.n + i];
+        b2 = max(b2, min(b1, x));
+        b1 = max(b1, x);
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+  for (int d = 1; d < per; d <<= 1) {
+    K c1, c2;
+    if constexpr (sizeof(K) == 8) {
+      c1 = __shfl_xor(static_cast<unsigned long long>(b1), d);
+      c2 = __shfl_xor(static_cast<unsigned long long>(b2), d);
+    } else {
+      c1 = __shfl_xor(static_cast<int>(b1), d);
+      c2 = __shfl_xor(static_cast<int>(b2), d);
+    }
+    b2 = max(max(b2, c2), min(b1, c1));
+    b1 = max(b1, c1);
+  }
+  return per;
+}
+
+// Whether the lane's group is among the top_groups best by `score` (the same in a group's `per` lanes; equal scores go
+// to the lower group): the groups ahead of it are counted.
+template <typename K>
+__device__ __forceinline__ bool group_stays(const RouteArgs& a, K score, int per) {
+  const int g = (threadIdx.x & 63) / per;
+  int ahead = 0;
+  for (int o = 0; o < a.groups; ++o) {
+    K s;
+    if constexpr (sizeof(K) == 8)
+      s = (static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(score >> 32), o * per))) << 32) |
+          static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(score), o * per));
+    else
+      s = __builtin_amdgcn_readlane(static_cast<int>(score), o * per);
+    ahead += (s > score || (s == score && o < g)) ? 1 : 0;
+  }
+  return g < a.groups && ahead < a.top_groups && score != 0;
+}
+
+// Takes the experts of groups that do not stay out of the keys.
+template <typename K, int NV>
+__device__ __forceinline__ void keep_groups(const RouteArgs& a, const Groups& gr, bool stays, int per, K (&key)[NV]) {
+  const int lane = threadIdx.x & 63;
+  if (gr.lanes) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) key[v] = stays ? key[v] : 0;
+    return;
+  }
+  const uint64_t who = __ballot(stays);
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int g = static_cast<int>(gr.by_n.div(min(lane * NV + v, a.experts - 1)));
+    if (!((who >> (g * per)) & 1)) key[v] = 0;
+  }
+}
+
+// Lane j's choice j in binary64: every score to 2^-50.
+template <int NV>
+__device__ __forceinline__ int choose_exactly(const RouteArgs& a, const Groups& gr, const float (&l)[NV], float m, uint64_t* mine) {
+  const int lane = threadIdx.x & 63;
+  double p[NV], sum = 0.0;
+  uint64_t key[NV], group[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    if (a.score == FP8RT_SOFTMAX) {
+      p[v] = exp(static_cast<double>(l[v]) - static_cast<double>(m));
+      sum += p[v];
+    } else {
+      p[v] = 1.0 / (1.0 + exp(-static_cast<double>(l[v])));
+    }
+  }
+  if (a.score == FP8RT_SOFTMAX) sum = wave_sum(sum);
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const bool there = l[v] > -INFINITY;
+    if (a.score == FP8RT_SOFTMAX) p[v] /= sum;
+    if (a.bias && there) p[v] += static_cast<double>(a.bias[lane * NV + v]);
+    group[v] = there ? rising(p[v]) : 0;
+    key[v] = a.bias ? group[v] : there ? rising(l[v]) : 0;
+  }
+  if (a.groups > 1) {
+    uint64_t b1, b2;
+    const int per = group_tops<uint64_t, NV>(a, gr, group, mine, b1, b2);
+    uint64_t score = b1;
+    if (a.group_best == 2 && b1) score = rising(number(b1) + (b2 ? number(b2) : 0.0));
+    keep_groups<uint64_t, NV>(a, gr, group_stays<uint64_t>(a, score, per), per, key);
+  }
+  int id = -1;
+  for (int j = 0; j < a.k; ++j) {
+    uint64_t best = 0;
+    int bv = 0, at;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+      if (key[v] > best) {
+        best = key[v];
+        bv = v;
+      }
+    if (wave_best(best, true, at) == 0) break;
+    const int v0 = __builtin_amdgcn_readlane(bv, at);  // (with all lanes on: inside the branch, bv would be computed there)
+    if (lane == j) id = at * NV + v0;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+      if (lane == at && v == bv) key[v] = 0;
+  }
+  return id;
+}
+
+// Lane j's choice j with 32-bit keys; `open` where their errors leave it undecided.  m: the largest logit; sum: of
+// e^(l - m), for a softmax whose scores are needed.
+template <int NV>
+__device__ __forceinline__ int choose(const RouteArgs& a, const Groups& gr, const float (&l)[NV], float m, float sum,
+                                      uint32_t* mine, bool& open) {
+  const int lane = threadIdx.x & 63;
+  const bool scores = a.bias || (a.groups > 1 && a.group_best == 2);
+  uint32_t key[NV], group[NV];
+  open = false;
+  // A score's error: the exponential (2 u and u of its argument, which weighs p by at most 1 / e), sum or quotient,
+  // product, 16 + 6 sums: 2^-19 of the largest score holds twice over, and the bias's sum adds u of the key.
+  float err = 0.0f;
+  if (scores) {
+    float p[NV];
+    const float inv = a.score == FP8RT_SOFTMAX ? __builtin_amdgcn_rcpf(sum) : 1.0f;
+    err = 0x1p-18f * inv;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      if (a.score == FP8RT_SOFTMAX)
+        p[v] = expf(l[v] - m) * inv;
+      else
+        p[v] = __builtin_amdgcn_rcpf(1.0f + expf(-l[v]));
+      const bool there = l[v] > -INFINITY;
+      if (a.bias && there) p[v] += a.bias[lane * NV + v];
+      group[v] = there ? rising32(p[v]) : 0;
+      key[v] = a.bias ? group[v] : there ? rising32(l[v]) : 0;
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) group[v] = key[v] = l[v] > -INFINITY ? rising32(l[v]) : 0;
+  }
+  if (a.groups > 1) {
+    uint32_t b1, b2;
+    const int per = group_tops<uint32_t, NV>(a, gr, group, mine, b1, b2);
+    uint32_t score = b1;
+    if (a.group_best == 2 && b1) score = rising32(number32(b1) + (b2 ? number32(b2) : 0.0f));
+    const bool stays = group_stays<uint32_t>(a, score, per);
+    if (scores && a.top_groups < a.groups) {  // the worst that stays against the best that goes
+      const float in = number32(~wave_max(stays ? ~score : 0u));
+      const uint32_t out = wave_max(stays || lane / per >= a.groups ? 0u : score);
+      const float gap = in - number32(out);
+      open = out != 0 && !(gap > 2.0f * err + 0x1p-20f * (fabsf(in) + fabsf(number32(b1)) + fabsf(number32(b2))));
+      open = __ballot(open) != 0;
+    }
+    keep_groups<uint32_t, NV>(a, gr, stays, per, key);
+  }
+  // the lane's keys in falling order (neighbours change places, so equal ones keep theirs); a round takes a lane's first
+  int at_v[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) at_v[v] = v;
+#pragma unroll
+  for (int r = 0; r < NV; ++r)
+#pragma unroll
+    for (int v = r & 1; v + 1 < NV; v += 2)
+      if (key[v + 1] > key[v]) {
+        const uint32_t x = key[v];
+        key[v] = key[v + 1];
+        key[v + 1] = x;
+        const int y = at_v[v];
+        at_v[v] = at_v[v + 1];
+        at_v[v + 1] = y;
+      }
+  int id = -1;
+  uint32_t last = 0;
+  const bool check = a.bias != nullptr;  // (logits are exact keys)
+  for (int j = 0; j < a.k + (check ? 1 : 0); ++j) {
+    const uint32_t top = wave_max(key[0]);
+    if (check && j > 0 && top != 0) {
+      const float x = number32(last), y = number32(top);
+      open = open || !(x - y > err + 0x1p-21f * (fabsf(x) + fabsf(y)));
+    }
+    last = top;
+    if (top == 0 || j == a.k) break;
+    const int at = __ffsll(static_cast<unsigned long long>(__ballot(key[0] == top))) - 1;
+    const int v0 = __builtin_amdgcn_readlane(at_v[0], at);
+    if (lane == j) id = at * NV + v0;
+    if (lane == at) {
+#pragma unroll
+      for (int v = 0; v + 1 < NV; ++v) {
+        key[v] = key[v + 1];
+        at_v[v] = at_v[v + 1];
+      }
+      key[NV - 1] = 0;
+    }
+  }
+  open = __ballot(open) != 0;
+  return id;
+}
+
+// Workgroup b takes tokens b plan.tokens ..; with one workgroup the plan is finished here.
 template <typename T, int NV>
-__global__ void __launch_bounds__(kThreads) k_route(RouteArgs a, Plan plan, FastDiv per_group) {
+__global__ void __launch_bounds__(kThreads) k_route(RouteArgs a, Plan plan, Groups gr) {
   __shared__ unsigned long long mask[kMaxE];
   __shared__ uint32_t base[kMaxE];
   __shared__ uint32_t part[kWaves];
   __shared__ int16_t chosen[kMaxTokens * kMaxK];
-  extern __shared__ uint64_t members[];  // [waves][experts], where there are groups
+  extern __shared__ uint64_t members[];  // [waves][experts], where groups are not runs of lanes
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int E = a.experts, k = a.k;
   const int64_t t0 = int64_t(blockIdx.x) * plan.tokens;
@@ -138,124 +388,42 @@ __global__ void __launch_bounds__(kThreads) k_route(RouteArgs a, Plan plan, Fast
     for (int e = threadIdx.x; e < E; e += kThreads) mask[e] = 0;
     __syncthreads();
   }
-  const bool wide = a.bias || (a.groups > 1 && a.group_best == 2);  // binary64 scores are needed
+  uint64_t* mine = members + wave * E;
   const T* logits = static_cast<const T*>(a.logits);
+  const bool summed = a.score == FP8RT_SOFTMAX && (a.bias || (a.groups > 1 && a.group_best == 2) || !a.renormalise);
+  float next[NV];
+  auto load = [&](int64_t t) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int e = lane * NV + v;
+      next[v] = e < E && t < a.tokens ? load_logit(logits + t * a.ld + e) : -INFINITY;
+    }
+  };
+  load(t0 + wave);
   for (int tt = wave; tt < plan.tokens; tt += kWaves) {
     const int64_t t = t0 + tt;
     if (t >= a.tokens) break;  // (uniform over the wave)
     float l[NV];
-    uint64_t key[NV];
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int e = lane * NV + v;
-      l[v] = e < E ? load_logit(logits + t * a.ld + e) : -INFINITY;
-    }
-    float top = l[0];
+    for (int v = 0; v < NV; ++v) l[v] = next[v];
+    if (tt + kWaves < plan.tokens) load(t + kWaves);  // in flight during this token's work
+    float m = -FLT_MAX, sum = 0.0f;
+    if (a.score == FP8RT_SOFTMAX) {
+      float top = l[0];
 #pragma unroll
-    for (int v = 1; v < NV; ++v) top = fmaxf(top, l[v]);
-    const float m = fmaxf(wave_max(top), -FLT_MAX);
-    uint64_t group[NV];  // what the groups are scored by
-    if (wide) {
-      double p[NV], sum = 0.0;
+      for (int v = 1; v < NV; ++v) top = fmaxf(top, l[v]);
+      m = fmaxf(wave_max(top), -FLT_MAX);
+      if (summed) {
 #pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        if (a.score == FP8RT_SOFTMAX) {
-          p[v] = exp(static_cast<double>(l[v]) - static_cast<double>(m));
-          sum += p[v];
-        } else {
-          p[v] = 1.0 / (1.0 + exp(-static_cast<double>(l[v])));
-        }
-      }
-      if (a.score == FP8RT_SOFTMAX) sum = wave_sum(sum);
-#pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        const int e = lane * NV + v;
-        const bool there = l[v] > -INFINITY;
-        if (a.score == FP8RT_SOFTMAX) p[v] /= sum;
-        if (a.bias && there) p[v] += static_cast<double>(a.bias[e]);
-        group[v] = there ? rising(p[v]) : 0;
-        key[v] = a.bias ? group[v] : there ? rising(l[v]) : 0;
-      }
-    } else {
-#pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        key[v] = l[v] > -INFINITY ? rising(l[v]) : 0;
-        group[v] = key[v];
+        for (int v = 0; v < NV; ++v) sum += expf(l[v] - m);
+        sum = wave_sum(sum);
       }
     }
-    if (a.groups > 1) {
-      // 64 / G' lanes a group (G' the next power of two) take its members in turn, then join
-      uint64_t* mine = members + wave * E;
-      int gp = 1;
-      while (gp < a.groups) gp <<= 1;
-      const int P = 64 / gp, g = lane / P, n = E / a.groups;
-#pragma unroll
-      for (int v = 0; v < NV; ++v)
-        if (lane * NV + v < E) mine[lane * NV + v] = group[v];
-      __builtin_amdgcn_wave_barrier();
-      uint64_t b1 = 0, b2 = 0;
-      if (g < a.groups) {
-        for (int i = lane - g * P; i < n; i += P) {
-          const uint64_t x = mine[g * n + i];
-          b2 = max(b2, min(b1, x));
-          b1 = max(b1, x);
-        }
-      }
-      for (int d = 1; d < P; d <<= 1) {
-        const uint64_t c1 = __shfl_xor(static_cast<unsigned long long>(b1), d);
-        const uint64_t c2 = __shfl_xor(static_cast<unsigned long long>(b2), d);
-        b2 = max(max(b2, c2), min(b1, c1));
-        b1 = max(b1, c1);
-      }
-      __builtin_amdgcn_wave_barrier();
-      uint64_t score = b1;
-      if (a.group_best == 2 && b1) score = rising(number(b1) + (b2 ? number(b2) : 0.0));
-      if (lane != g * P) score = 0;
-      uint64_t stay = 0;
-      for (int i = 0; i < a.top_groups; ++i) {
-        int at;
-        if (wave_best(score, wide, at) == 0) break;
-        stay |= uint64_t(1) << (at / P);
-        if (lane == at) score = 0;
-      }
-#pragma unroll
-      for (int v = 0; v < NV; ++v)
-        if (!((stay >> per_group.div(min(lane * NV + v, E - 1))) & 1)) key[v] = 0;
-    }
-    // the lane's own best, and k rounds over the wave; lane j keeps choice j
-    uint64_t best = 0;
-    int bv = 0;
-    float bl = 0.0f;
-    auto own = [&] {
-      best = 0;
-#pragma unroll
-      for (int v = 0; v < NV; ++v)
-        if (key[v] > best) {
-          best = key[v];
-          bv = v;
-          bl = l[v];
-        }
-    };
-    own();
-    int id = -1;
-    float chosen_l = 0.0f;
-    for (int j = 0; j < k; ++j) {
-      int at;
-      if (wave_best(best, a.bias != nullptr, at) == 0) break;
-      const int v = __builtin_amdgcn_readlane(bv, at);
-      const float lv = __uint_as_float(__builtin_amdgcn_readlane(static_cast<int>(__float_as_uint(bl)), at));
-      if (lane == j) {
-        id = at * NV + v;
-        chosen_l = lv;
-      }
-      if (lane == at) {
-#pragma unroll
-        for (int u = 0; u < NV; ++u)
-          if (u == bv) key[u] = 0;
-        own();
-      }
-    }
+    bool open;
+    int id = choose<NV>(a, gr, l, m, sum, reinterpret_cast<uint32_t*>(mine), open);
+    if (open) id = choose_exactly<NV>(a, gr, l, m, mine);
     const bool there = id >= 0;
+    const float chosen_l = there ? load_logit(logits + t * a.ld + id) : 0.0f;
     float w;
     if (a.renormalise) {
       const float q = relative(chosen_l, there, a.score);
@@ -264,10 +432,7 @@ __global__ void __launch_bounds__(kThreads) k_route(RouteArgs a, Plan plan, Fast
     } else if (a.score == FP8RT_SIGMOID) {
       w = 1.0f / (1.0f + expf(-chosen_l));
     } else {
-      float sum = 0.0f;
-#pragma unroll
-      for (int v = 0; v < NV; ++v) sum += expf(l[v] - m);
-      w = expf(chosen_l - m) / wave_sum(sum);
+      w = expf(chosen_l - m) / sum;
     }
     if (lane < k) {
       a.ids[t * k + lane] = id;
@@ -459,17 +624,21 @@ hipError_t launch_expert_route(const RouteArgs& a, hipStream_t st) {
     if (e != hipSuccess) return e;
     plan.counts = static_cast<uint8_t*>(p);
   }
-  const size_t lds = a.groups > 1 ? size_t(kWaves) * a.experts * sizeof(uint64_t) : 0;
-  const FastDiv per_group(static_cast<uint32_t>(a.experts / a.groups));
   hipError_t e = hipSuccess;
   by_width(a.experts, [&](auto nv) {
     constexpr int NV = decltype(nv)::value;
+    Groups gr{};
+    gr.n = a.experts / a.groups;
+    gr.by_n = FastDiv(static_cast<uint32_t>(gr.n));
+    gr.lanes = gr.n % NV == 0 ? gr.n / NV : 0;
+    if (gr.lanes & (gr.lanes - 1)) gr.lanes = 0;
+    const size_t lds = a.groups > 1 && !gr.lanes ? size_t(kWaves) * a.experts * sizeof(uint64_t) : 0;
     auto go = [&](auto kern) {
       if (lds > 32768) {  // (beside the static arrays, past the default limit)
         e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds));
         if (e != hipSuccess) return;
       }
-      hipLaunchKernelGGL(kern, dim3(plan.blocks), dim3(kThreads), lds, st, a, plan, per_group);
+      hipLaunchKernelGGL(kern, dim3(plan.blocks), dim3(kThreads), lds, st, a, plan, gr);
     };
     a.lt == FP8RT_BF16 ? go(k_route<uint16_t, NV>) : go(k_route<float, NV>);
   });
