@@ -932,6 +932,7 @@ fp8rt_status fp8_gated_backward(const void* dz, fp8rt_dtype t, int64_t rows, int
   if (ldk % 16 != 0 || lddx % 16 != 0 || (z && ldz % 16 != 0)) return FP8RT_EALIGN;
   if (!aligned16(kept) || !aligned16(dx) || !aligned16(z) || !aligned4(kept_scale) || !aligned4(live))
     return FP8RT_EALIGN;
+  if (cols > kGatedMaxCols) return FP8RT_EUNSUPPORTED;
   GatedArgs a;
   a.x = dz;
   a.xt = t;

@@ -94,6 +94,7 @@ __device__ __forceinline__ bool find_unit(const ExpertGemmArgs& g, int b, int co
       const int at = __ffsll(static_cast<unsigned long long>(past)) - 1;
       const int rows = __builtin_amdgcn_readlane(n, at);
       index -= __builtin_amdgcn_readlane(s, at) - rows * col_tiles;
+      if (index < 0 || index >= rows * col_tiles) return false;  // (sums of claims on the same slots may wrap)
       const int first = index / (4 * col_tiles) * 4, in = index - first * col_tiles, m = min(4, rows - first);
       t.expert = e0 + at;
       t.row0 = __builtin_amdgcn_readlane(lo, at) + static_cast<int64_t>(first + in % m) * TM;
@@ -283,11 +284,21 @@ __device__ __forceinline__ i32x8 frag_a(const TileOperands& p, const TileShared<
   return join(*reinterpret_cast<const u32x4*>(at + p.lo), *reinterpret_cast<const u32x4*>(at + p.hi));
 }
 
-// Stage s: B's fragments in bc.  kRound: the loads of stage s + 3 of A and s + 2 of B (to bn) are issued; kMore: all loads
+// As mfma16, with b in AGPRs: loads write them directly, and a wave of 256 registers has too few of the others for three
+// sets of B beside A's fragments (a set that the compiler moved there by itself was waited for as soon as it was loaded).
+template <int FA>
+__device__ __forceinline__ void mfma16_ab(f32x4& acc, const i32x8& b, const i32x8& a) {
+  if constexpr (FA == 0)
+    asm volatile("v_mfma_f32_16x16x128_f8f6f4 %0, %1, %2, %0" : "+a"(acc) : "a"(b), "v"(a));
+  else
+    asm volatile("v_mfma_f32_16x16x128_f8f6f4 %0, %1, %2, %0 blgp:1" : "+a"(acc) : "a"(b), "v"(a));
+}
+
+// Stage s: B's fragments in bc (AB: in AGPRs).  kRound: the loads of stage s + 3 of A and s + 2 of B (to bn) are issued; kMore: all loads
 // have been, a stage may follow; kEnd: none does.  (The barrier's count is that of the loads issued after those of stage
 // s + 1 of A, which it waits for: a stage issues B's 8 before its barrier and A's 2 NB after it.)
 enum StageKind { kRound, kMore, kEnd };
-template <int FA, int NB, StageKind KIND, int BLOCKS>
+template <int FA, int NB, StageKind KIND, bool AB, int BLOCKS>
 __device__ __forceinline__ void tile_stage(const TileOperands& p, TileShared<BLOCKS>& sh, int s, f32x4 (&acc)[NB][4][4],
                                            i32x8 (&af)[4], const i32x8 (&bc)[4], i32x8 (&bn)[4]) {
   constexpr int MI = 4 * NB;
@@ -296,7 +307,10 @@ __device__ __forceinline__ void tile_stage(const TileOperands& p, TileShared<BLO
     if (i == MI / 2 && KIND != kEnd) stage_barrier<(KIND == kRound ? 16 : 8) + 2 * NB>();
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      mfma16<FA>(acc[i / 4][i & 3][j], bc[j], af[i & 3]);
+      if constexpr (AB)
+        mfma16_ab<FA>(acc[i / 4][i & 3][j], bc[j], af[i & 3]);
+      else
+        mfma16<FA>(acc[i / 4][i & 3][j], bc[j], af[i & 3]);
       if (j == 0 && i + 2 < MI) af[(i + 2) & 3] = frag_a(p, sh, i + 2, s);
       if (j == 0 && i + 2 >= MI && KIND != kEnd) af[(i + 2) & 3] = frag_a(p, sh, i + 2 - MI, s + 1);
       if (KIND == kRound) {
@@ -333,12 +347,12 @@ __device__ __forceinline__ void tile_body(const ExpertGemmArgs& g, TileShared<BL
   const int ns = p.last + 1;
   int s = 0;
   for (; s + 3 <= ns; s += 3) {
-    tile_stage<FA, NB, kRound>(p, sh, s, acc, af, b0, b2);
-    tile_stage<FA, NB, kRound>(p, sh, s + 1, acc, af, b1, b0);
-    tile_stage<FA, NB, kRound>(p, sh, s + 2, acc, af, b2, b1);
+    tile_stage<FA, NB, kRound, false>(p, sh, s, acc, af, b0, b2);
+    tile_stage<FA, NB, kRound, false>(p, sh, s + 1, acc, af, b1, b0);
+    tile_stage<FA, NB, kRound, BLOCKS == 1>(p, sh, s + 2, acc, af, b2, b1);
   }
-  if (s < ns) tile_stage<FA, NB, kMore>(p, sh, s, acc, af, b0, b2);
-  if (s + 1 < ns) tile_stage<FA, NB, kEnd>(p, sh, s + 1, acc, af, b1, b0);
+  if (s < ns) tile_stage<FA, NB, kMore, false>(p, sh, s, acc, af, b0, b2);
+  if (s + 1 < ns) tile_stage<FA, NB, kEnd, false>(p, sh, s + 1, acc, af, b1, b0);
 #pragma unroll
   for (int b = 0; b < NB; ++b) fence16(acc[b]);
   step_barrier<0>();  // every load has landed and every fragment is read: the ring is free
@@ -452,16 +466,21 @@ __global__ void __launch_bounds__(kTileThreads, BLOCKS == 4 ? 1 : 2) k_expert_ti
 }  // namespace
 
 // Which kernel.  The host knows the slots and the experts, not how the plan shares them out, so the rule goes by the
-// average a = slots / experts and by the units that the tile kernel would have at most.  Measured with equal
-// experts, N x K, us (stream of 16 / of 32 slots, tiles of 64 / of 256; the weights alone at 6.1 TB/s):
-//   4096 x 7168,  32 experts of  4 slots: 139 / 144, 160 / 160 (154)      of 16: 169 / 153, 162 / 162
-//   7168 x 2048,  32 experts of  8 slots:  88 /  98,  87 /  92  (77)      of 32: 170 / 110,  92 /  98
-//   4096 x 7168,   8 experts of 16 slots:  44 /  44,  62 /  53  (38)      of 32:  67 /  54,  64 /  55  (128 units)
-//   4096 x 7168,   2 experts of 16 slots:  14 /  16,  37 /  27  (10)      of 32:  25 /  17,  37 /  28   (32 units)
-//   4096 x 7168,  32 experts of 64 slots: tiles of 64 / of 256 169 / 171, of 128: 221 / 190
-//   2048 x 2048, 128 experts of 64 slots: 106 / 113, of 128: 142 / 138;  8 experts of 64, 4096 x 7168 (128 units): 67 / 59
-// A few slots an expert are streamed; from 9 on tiles win where they fill the CUs, from 33 on always.  Tiles of
-// 64 (two workgroups a CU) up to 64 slots where there are units for both.
+// average a = slots / experts and by the units that the tile kernel would have at least.  Measured, experts x slots of each,
+// us (the weights alone at 6.1 TB/s in brackets):
+//   stream of 16 slots / of 32, tiles of 64 / of 256
+//     4096 x 7168:  32 x 4 139 / 144, 159 / 160 (154);  32 x 16 169 / 153, 161 / 163;  8 x 16 44 / 44, 52 / 53 (38);
+//                   8 x 32 67 / 54, 54 / 55;  2 x 16 14 / 16, 27 / 27 (10);  2 x 32 25 / 17, 27 / 27
+//     7168 x 2048:  32 x 8 88 / 98, 88 / 92 (77);  32 x 32 170 / 110, 92 / 98
+//   tiles of 64 / of 256
+//     4096 x 7168:  32 x 64 169 / 171, 32 x 128 213 / 190;  8 x 64 58 / 59, 8 x 128 59 / 67, 8 x 160 84 / 73
+//     4096 x 4096:  32 x 88 121 / 107, of 32 with 96 on average but unequal 131 / 139;  8 x 88 30 / 37
+//     7168 x 2048:  32 x 88 112 / 116, of 88 on average but unequal 124 / 142;  32 x 128 118 / 121, 32 x 256 182 / 154
+//     4096 x 1024:  32 x 128 43 / 48, 32 x 192 59 / 58, of 178 on average but unequal 58 / 68
+// A few slots an expert are streamed, up to 32 where tiles would not fill the CUs.  Tiles of 256 read the weights
+// from the L2 cache a quarter as often; those of 64, two workgroups a CU, waste less of a CU on starts, ends, partial tiles and
+// uneven shares.  So the latter take up to 64 slots, more the shorter their loops (a K up to 2^18) and up to 128 where all of
+// them run at once.
 hipError_t launch_expert_gemm(const ExpertGemmArgs& g, hipStream_t st) {
   const FastDiv choices(static_cast<uint32_t>(g.choices));
   const int64_t a = ceil_div(g.slots, g.experts), col_tiles = ceil_div(g.N, kTN), cus = device_cus();
@@ -488,7 +507,7 @@ hipError_t launch_expert_gemm(const ExpertGemmArgs& g, hipStream_t st) {
     const int64_t units = std::min(g.experts, g.slots) * col_tiles;
     if (a <= 8 || (a <= 16 && units < cus)) return stream(fa, o, integral_constant<int, 1>{}, integral_constant<int, 1>{});
     if (a <= 32 && units < cus) return stream(fa, o, integral_constant<int, 2>{}, integral_constant<int, 2>{});
-    if (a <= 64 && units >= 2 * cus) return tile(fa, o, integral_constant<int, 1>{});
+    if (a <= 64 || a * g.K <= (int64_t(1) << 18) || (a <= 128 && units <= cus)) return tile(fa, o, integral_constant<int, 1>{});
     tile(fa, o, integral_constant<int, 4>{});
   };
   auto by_out = [&](auto fa) { g.yt == FP8RT_BF16 ? by_rows(fa, uint16_t{}) : by_rows(fa, float{}); };

@@ -410,9 +410,8 @@ hipError_t launch_gated_quantize(const GatedArgs& a, hipStream_t st) {
   const int64_t run = std::max<int64_t>(a.er == 1 ? a.ec >> 3 : 1, kKeptRun);
   const int64_t opad = ceil_div(octets, run) * run;
   // about four octets a thread; at most kMaxBlocks workgroups, one partial each (opad <= 8192 and
-  // rows_per <= 2^18 rows keep a workgroup's count of octets in 32 bits)
+  // rows_per <= 2^18 keep a workgroup's count of octets in 32 bits)
   const int64_t rows_per = std::max(ceil_div(1024, opad), ceil_div(a.rows, kMaxBlocks));
-  if (rows_per * opad >= (int64_t(1) << 32)) return hipErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(ceil_div(a.rows, rows_per)));
   by_kind(a, [&](auto t, auto f, auto act, auto kept) {
     hipLaunchKernelGGL((k_gated_groups<decltype(t), decltype(f)::value, decltype(act)::value, decltype(kept)::value>), grid,
@@ -425,9 +424,8 @@ hipError_t launch_gated_quantize(const GatedArgs& a, hipStream_t st) {
 
 hipError_t launch_gated_backward(const GatedArgs& a, hipStream_t st) {
   const int64_t octets = a.cols >> 3;
-  // about two octets a thread; at most 2^20 workgroups
+  // about two octets a thread; at most 2^20 workgroups (of at most 2^11 rows of 2^13 octets)
   const int64_t rows_per = std::max(ceil_div(512, octets), ceil_div(a.rows, int64_t(1) << 20));
-  if (rows_per * octets >= (int64_t(1) << 32)) return hipErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(ceil_div(a.rows, rows_per)));
   auto go = [&](auto kern) {
     hipLaunchKernelGGL(kern, grid, dim3(256), 0, st, a, static_cast<int>(rows_per), FastDiv(static_cast<uint32_t>(octets)));

@@ -22,7 +22,8 @@
  *        (ceil(M/256) * 256 * K/128 * 4 bytes), the FP32 parts of a last wave
  *        split along K (up to 4 parts x 256 KB per split 256 x 256 tile), the
  *        cast-transpose's per-group arrays, the ledger's partials, the shares of
- *        a norm's weight gradient and the parts of attention cut along its keys.  When a
+ *        a norm's weight gradient, the parts of attention cut along its keys and
+ *        the router's counts.  When a
  *        call needs more, a larger buffer (at least twice the old) is
  *        allocated and the old one is KEPT, never freed: every address handed
  *        to a kernel stays valid for the process's life.
@@ -631,8 +632,8 @@ fp8rt_status fp8_expert_route_backward(const void* logits, fp8rt_dtype lt, int64
  *   slots : rows of y (and entries of order), a bound on offsets[experts]
  *   y  : [slots x N] bf16 / fp32 (ldy); rows of no expert are left as they were
  * The device's integers are not trusted: offsets are clamped to [0, slots], an expert whose end lies before its
- * start has no slots, and of two experts that claim one slot either may write it; a slot whose r lies outside
- * [0, a_rows) is 0.
+ * start has no slots, and where experts claim the same slots it is open which of the claims are served; a slot
+ * whose r lies outside [0, a_rows) is 0.
  * Format pairs: E4M3 x E4M3 and E5M2 x E4M3 (a data gradient: the same call with the K-major weights).
  * Granularities: ga row {1,0} or tensor {0,0}; gb channel {1,0}, expert {N,0} or tensor {0,0}; else
  * FP8RT_EUNSUPPORTED.  flags: FP8RT_B_PACKED16, which is required (without it FP8RT_EUNSUPPORTED: decode and
@@ -675,7 +676,8 @@ fp8rt_status fp8_gated_quantize(const void* x, fp8rt_dtype xt, int64_t rows, int
  *   z  : nullable [rows x cols] of type t (ldz): the activation computed again, for the down projection's weight
  *        gradient
  *   kept, kf, ldk, kept_scale, live : as fp8_gated_quantize
- * Alignment: cols and leading dimensions multiples of 16, matrices 16-byte aligned. */
+ * Alignment: cols and leading dimensions multiples of 16, matrices 16-byte aligned.  cols <= 65536, else
+ * FP8RT_EUNSUPPORTED. */
 fp8rt_status fp8_gated_backward(const void* dz, fp8rt_dtype t, int64_t rows, int64_t cols, int64_t lddz,
                                 const uint8_t* kept, fp8rt_format kf, int64_t ldk, const float* kept_scale,
                                 fp8rt_act act, void* dx, int64_t lddx, void* z, int64_t ldz, const int32_t* live,

@@ -139,6 +139,7 @@ def gated_grad(rt, **kw):
     (dict(lddz=264), "EALIGN"), (dict(ldk=520), "EALIGN"), (dict(lddx=520), "EALIGN"), (dict(ldz=264), "EALIGN"),
     (dict(dz=FAKE + 8), "EALIGN"), (dict(kept=FAKE + 8), "EALIGN"), (dict(dx=FAKE + 8), "EALIGN"),
     (dict(z=FAKE + 8), "EALIGN"), (dict(ks=FAKE + 2), "EALIGN"), (dict(live=FAKE + 2), "EALIGN"),
+    (dict(cols=65552, lddz=65552, ldk=131104, lddx=131104, ldz=65552), "EUNSUPPORTED"),
 ])
 def test_gated_gradient_refusals(rt, kw, status):
     assert gated_grad(rt, **kw) == getattr(rt, status)

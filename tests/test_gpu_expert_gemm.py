@@ -68,6 +68,15 @@ def test_rows_of_an_expert(rt, rows):
     check(rt, (rows, 0, rows // 2, rows), 272, 384, gather=True, choices=2)
 
 
+@pytest.mark.parametrize("kw", [dict(), dict(fa=1, out=torch.float32, gather=True, choices=3, pad=32),
+                                dict(out=torch.float32, ga=(0, 0), gb="expert"), dict(fa=1, gather=True, spare=9, gb="tensor")])
+@pytest.mark.parametrize("counts", [(150, 140), (300, 70, 200, 130, 240), (257, 1, 300)])
+@pytest.mark.parametrize("N", [16, 272])
+def test_many_rows_and_deep(rt, counts, N, kw):
+    """The tiles of 256 slots, with each number of blocks of 64."""
+    check(rt, counts, N, 2176, **kw)
+
+
 @pytest.mark.parametrize("fa", [0, 1])
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("ga", [(1, 0), (0, 0)])
