@@ -26,7 +26,7 @@ namespace fp8rt {
 
 namespace {
 
-constexpr int kThreads = 512;       // of k_route: more would leave its 64-bit path too few registers
+constexpr int kThreads = 512;       // of k_route; up to 1024 where its 64-bit path has registers enough for them
 constexpr int kPlanThreads = 1024;  // of k_route_plan
 constexpr int kMaxE = static_cast<int>(kRouteMaxExperts), kMaxK = static_cast<int>(kRouteMaxK);
 constexpr int kMaxTokens = 64;  // of a workgroup
@@ -443,7 +443,7 @@ __device__ __forceinline__ Settled choose(const RouteArgs& a, const Groups& gr, 
 
 // Workgroup b takes tokens b plan.tokens ..; with one workgroup the plan is finished here.
 template <typename T, int L, int NV>
-__global__ void __launch_bounds__(kThreads) k_route(RouteArgs a, Plan plan, Groups gr) {
+__global__ void __launch_bounds__(NV <= 4 ? 2 * kThreads : kThreads) k_route(RouteArgs a, Plan plan, Groups gr) {
   __shared__ unsigned long long mask[kMaxE];
   __shared__ uint32_t base[kMaxE];
   __shared__ uint32_t part[kThreads / 64];
@@ -454,13 +454,13 @@ __global__ void __launch_bounds__(kThreads) k_route(RouteArgs a, Plan plan, Grou
   const int64_t t0 = int64_t(blockIdx.x) * plan.tokens;
   const bool planned = a.slots != nullptr;
   if (planned) {
-    for (int e = threadIdx.x; e < E; e += kThreads) mask[e] = 0;
+    for (int e = threadIdx.x; e < E; e += blockDim.x) mask[e] = 0;
     __syncthreads();
   }
   uint64_t* mine = members + run * E;
   const T* logits = static_cast<const T*>(a.logits);
   const bool summed = a.score == FP8RT_SOFTMAX && (a.bias || (a.groups > 1 && a.group_best == 2) || !a.renormalise);
-  for (int tt = run; tt < plan.tokens; tt += kThreads / L) {  // (the same rounds in every run)
+  for (int tt = run; tt < plan.tokens; tt += blockDim.x / L) {  // (the same rounds in every run)
     const int64_t t = t0 + tt;
     const bool live = t < a.tokens;
     if (__ballot(live) == 0) break;
@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(kThreads) k_route(RouteArgs a, Plan plan, Grou
   }
   if (!planned) return;
   __syncthreads();
-  if (plan.blocks == 1) {  // thread t: experts 2 t and 2 t + 1
+  if (plan.blocks == 1) {  // kThreads of them, thread t for experts 2 t and 2 t + 1
     static_assert(2 * kThreads >= kMaxE, "an expert for every half thread");
     const int e = 2 * threadIdx.x;
     const uint32_t n0 = e < E ? __popcll(mask[e]) : 0u, n1 = e + 1 < E ? __popcll(mask[e + 1]) : 0u;
@@ -529,11 +529,11 @@ __global__ void __launch_bounds__(kThreads) k_route(RouteArgs a, Plan plan, Grou
     if (threadIdx.x == 0) a.offsets[E] = static_cast<int32_t>(all);
     __syncthreads();
   } else {
-    for (int e = threadIdx.x; e < E; e += kThreads)
+    for (int e = threadIdx.x; e < E; e += blockDim.x)
       plan.counts[int64_t(blockIdx.x) * plan.pitch + e] = static_cast<uint8_t>(__popcll(mask[e]));
   }
   const int64_t here = min(static_cast<int64_t>(plan.tokens), a.tokens - t0);
-  for (int i = threadIdx.x; i < here * k; i += kThreads) {
+  for (int i = threadIdx.x; i < here * k; i += blockDim.x) {
     const int tt = i / k, e = chosen[i + 2 * tt];
     int32_t slot = -1;
     if (e >= 0) {
@@ -704,11 +704,16 @@ hipError_t launch_expert_route(const RouteArgs& a, hipStream_t st) {
   hipError_t e = hipSuccess;
   by_width(a.experts, a.k, groups_p2, [&](auto l, auto nv) {
     constexpr int L = decltype(l)::value, NV = decltype(nv)::value;
-    // One workgroup finishes the plan of up to 64 tokens by itself.  Else 32 each, so that a few thousand tokens reach
-    // every CU (16 each: 4096 tokens 9.9 us and their plan 9.2, against 7.6 and 6.4: twice the counts to sum); beyond
-    // that 64, the most that a mask holds, for half the counts.
-    plan.tokens = a.tokens <= kMaxTokens || a.tokens > 16384 ? kMaxTokens : 32;
+    // One workgroup finishes the plan by itself where its runs take at most two rounds (the plan's launch costs about as
+    // much as a round).  Else about 256 workgroups, each of at least a round of kThreads (4096 tokens of 16 lanes in
+    // 256 blocks of 16: 9.9 us and their plan 9.2, in 128 of 32: 7.6 and 6.4) and of at most a mask's 64 tokens.
+    constexpr int kRuns = kThreads / L;
+    if (a.tokens <= 2 * kRuns)
+      plan.tokens = 2 * kRuns;
+    else
+      for (plan.tokens = kRuns; plan.tokens < kMaxTokens && plan.tokens * 256 < a.tokens;) plan.tokens *= 2;
     plan.blocks = static_cast<int>(ceil_div(a.tokens, plan.tokens));
+    const int threads = plan.blocks == 1 ? kThreads : std::min(plan.tokens * L, NV <= 4 ? 2 * kThreads : kThreads);
     if (a.slots && plan.blocks > 1) {
       void* p = nullptr;
       e = get_scratch(st, size_t(plan.blocks) * plan.pitch, &p);
@@ -720,13 +725,13 @@ hipError_t launch_expert_route(const RouteArgs& a, hipStream_t st) {
     gr.by_n = FastDiv(static_cast<uint32_t>(gr.n));
     gr.lanes = gr.n % NV == 0 ? gr.n / NV : 0;
     if (gr.lanes & (gr.lanes - 1)) gr.lanes = 0;
-    const size_t lds = a.groups > 1 && !gr.lanes ? size_t(kThreads / L) * a.experts * sizeof(uint64_t) : 0;
+    const size_t lds = a.groups > 1 && !gr.lanes ? size_t(threads / L) * a.experts * sizeof(uint64_t) : 0;
     auto go = [&](auto kern) {
       if (lds > 32768) {  // (beside the static arrays, past the default limit)
         e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds));
         if (e != hipSuccess) return;
       }
-      hipLaunchKernelGGL(kern, dim3(plan.blocks), dim3(kThreads), lds, st, a, plan, gr);
+      hipLaunchKernelGGL(kern, dim3(plan.blocks), dim3(threads), lds, st, a, plan, gr);
     };
     a.lt == FP8RT_BF16 ? go(k_route<uint16_t, L, NV>) : go(k_route<float, L, NV>);
   });

@@ -604,7 +604,7 @@ typedef FP8RT_ENUM(fp8rt_act) { FP8RT_SILU = 0, FP8RT_GELU = 1 } fp8rt_act;
  *   slots   : slots[t,j], the slot of that choice
  * experts <= 1024, k <= 32, groups <= 64 (else FP8RT_EUNSUPPORTED); groups divides experts; k <= experts / groups *
  * top_groups; tokens * k < 2^31; scale finite.  Alignment: pointers to their element.
- * Scratch: the per-stream scratch buffer holds experts bytes for each 32 tokens. */
+ * Scratch: the per-stream scratch buffer holds up to experts bytes for each 8 tokens. */
 fp8rt_status fp8_expert_route(const void* logits, fp8rt_dtype lt, int64_t tokens, int64_t experts, int64_t ld,
                               fp8rt_score score, const float* bias, int64_t groups, int64_t top_groups,
                               int64_t group_best, int64_t k, int32_t renormalise, float scale, int32_t* ids,
