@@ -3,8 +3,8 @@
 //
 //   y[t] = residual[t] + sum_j w[t,j] x[slot(t,j)];   dx[slot(t,j)] = w[t,j] dy[t],   dw[t,j] = <dy[t], x[slot(t,j)]>
 //
-// Bound by memory: every row once (4096 tokens of 8 x 7168 bf16: 587 MB forward, 998 back).  Measured: 120 us (4.9 TB/s)
-// and 204 us (4.9 TB/s, as much as a large copy reaches); a step of 64 tokens 4.9 us, of which a launch is 3.
+// Bound by memory: every row once (4096 tokens of 8 x 7168 bf16: 587 MB forward, 998 back).  Measured: 126 us (4.7 TB/s)
+// and 201 us (5.0 TB/s; a large copy reaches 4.8); a step of 64 tokens 4.9 us, of which a launch is 3.
 #include <algorithm>
 
 #include "device_common.h"

@@ -10,8 +10,8 @@
 // a 64-bit mask; a choice's place among its expert's is the number of set bits below its token (stable and free of
 // atomics on counters), and a workgroup's count is the mask's population.
 //
-// Measured (kernels alone): a token of 64 experts 4.6 us, of which a launch is 3; 4096 tokens of 64 (k 6, bf16) 7.6 us, their
-// plan 5 to 6, the gradient 4.9; 8192 of 256 (k 8 of 4 of 8 groups, biased sigmoids) 18 us and the plan 5.9.  The bytes
+// Measured (kernels alone): a token of 64 experts 4.6 us, of which a launch is 3; 4096 tokens of 64 (k 6, bf16) 7.3 us, their
+// plan 4.7, the gradient 4.9; 8192 of 256 (k 8 of 4 of 8 groups, biased sigmoids) 18 us and the plan 5.9.  The bytes
 // (8 MiB of logits there) would take 2 us: what bounds it is the chain of k + 2 rounds of a maximum over the token's lanes, of 10
 // to 14 dependent instructions each, hidden by the other waves of a SIMD.  Bounds of 8 waves a SIMD spill (30 us).
 #include <float.h>
@@ -678,8 +678,8 @@ __global__ void __launch_bounds__(256) k_route_backward(RouteArgs a) {
 }
 
 // Lanes of a token and experts of a lane: as few lanes as hold the experts 4 each, at least one for each group, choice
-// and the two behind the choices.  (256 experts, 8 groups, 8192 tokens: 64 lanes of 4 take 18 us, 32 lanes of 8 23: the
-// choice in binary64 of the one token in thousands that needs it costs them a third of their waves.)
+// and the two behind the choices.  (256 experts, 8 groups, 8192 tokens: 64 lanes of 4 take 18 us, 32 lanes of 8 23: they
+// need half as many registers again.)
 template <typename F>
 void by_width(int experts, int k, int groups, F&& f) {
   using std::integral_constant;
