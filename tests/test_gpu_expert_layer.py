@@ -10,6 +10,7 @@ import os
 import sys
 
 import pytest
+import torch
 
 pytestmark = pytest.mark.gpu
 
@@ -26,3 +27,32 @@ def test_layer_and_gradients(shape):
     *errors, router = expert_layer.main(**shape)
     outputs, grads = errors[::2], errors[1::2]
     assert max(outputs) < 0.12 and max(grads) < 0.18 and router < 0.12
+
+
+@pytest.mark.parametrize("tokens", [1, 150])
+def test_captured_and_replayed(tokens):
+    """The layer in one graph, replayed on new inputs with eager work on another stream in between: as without it, bit for bit."""
+    import expert_layer
+
+    layer = expert_layer.Experts(512, 256, 16, 4)
+    g = torch.Generator().manual_seed(tokens)
+    inputs = [[torch.randn(tokens, 512, generator=g).bfloat16().cuda() for _ in range(2)] for _ in range(4)]
+    want = [layer(*i)[0].clone() for i in inputs]
+    x, res = (t.clone() for t in inputs[0])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        layer(x, res)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        y = layer(x, res)[0]
+    for i in (1, 2, 3, 0):
+        x.copy_(inputs[i][0])
+        res.copy_(inputs[i][1])
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            graph.replay()
+        other = layer(*inputs[(i + 1) % 4])[0]  # this stream's own memory
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[i]) and torch.equal(other, want[(i + 1) % 4])

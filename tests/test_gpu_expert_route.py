@@ -75,6 +75,15 @@ def test_tokens(rt, tokens):
     check(rt, logits_of(tokens, 256, seed=3), 8, score="sigmoid", groups=8, top=4, best=2, bias=logits_of(1, 256)[0] * 0.05)
 
 
+@pytest.mark.parametrize("tokens,experts,k,kw", [
+    (700, 600, 5, dict(score="sigmoid")), (2500, 200, 6, dict(groups=2, top=1, best=2)), (5000, 256, 3, dict()),
+    (4200, 40, 4, dict(groups=5, top=2, best=2)), (1500, 120, 9, dict(score="sigmoid", groups=3, top=2))])
+def test_blocks_of_tokens(rt, tokens, experts, k, kw):
+    """Blocks of 8, 16 and 32 tokens, one and two rounds of a workgroup's runs; groups that are no runs of lanes."""
+    bias = logits_of(1, experts, seed=5)[0] * 0.02
+    check(rt, logits_of(tokens, experts, seed=9), k, bias=bias, **kw)
+
+
 def test_many_tokens(rt):
     """More than 256 workgroups, blocks of 32 and of 64 tokens: the plan against a stable sort of the ids."""
     for tokens, experts, k in ((16385, 8, 2), (9000, 64, 6), (40000, 16, 4), (70001, 128, 1)):

@@ -89,6 +89,16 @@ def test_granularities(rt, gran, dtype, fmt, act):
     check(rt, 2, 2048, dtype=dtype, gran=gran, fmt=fmt, act=act, mode=mode, keep=False)
 
 
+@pytest.mark.parametrize("gran", [(1, 16), (1, 128), (1, 512), (0, 0)])
+@pytest.mark.parametrize("cols", [4096, 4112, 8208, 20000])
+def test_few_wide_rows(rt, gran, cols):
+    """Rows that are cut into chunks, whole and not, with groups short at the row's end."""
+    mode = rt.GIVEN if gran == (0, 0) else rt.DYNAMIC
+    check(rt, 5, cols, gran=gran, mode=mode, pad=16)
+    check(rt, 7, cols, gran=gran, mode=mode, act=1, keep=False, live=None if gran == (0, 0) else 4)
+    check_grad(rt, 6, cols, act=1, pad=16, live=4)
+
+
 @pytest.mark.parametrize("gran", [(1, 0), (1, 32), (1, 128)])
 def test_given_and_pow2(rt, gran):
     check(rt, 33, 784, gran=gran, mode=rt.GIVEN)
