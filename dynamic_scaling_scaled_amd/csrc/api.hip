@@ -740,6 +740,8 @@ fp8rt_status route_setup(const void* logits, fp8rt_dtype lt, int64_t tokens, int
   if (tokens <= 0 || experts <= 0 || k <= 0 || ld < experts || k > experts || !isfinite(scale)) return FP8RT_EINVAL;
   if (experts > kRouteMaxExperts || k > kRouteMaxK) return FP8RT_EUNSUPPORTED;
   if (tokens >= kInt31 || tokens * k >= kInt31 || ld >= kInt31) return FP8RT_EINVAL;
+  // a workgroup of up to 1024 threads for every 64 tokens: at most 2^31 threads
+  if (tokens > (int64_t(1) << 27)) return FP8RT_EUNSUPPORTED;
   if (reinterpret_cast<uintptr_t>(logits) & (lt == FP8RT_F32 ? 3u : 1u)) return FP8RT_EALIGN;
   a.logits = logits;
   a.lt = lt;

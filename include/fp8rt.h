@@ -602,7 +602,7 @@ typedef FP8RT_ENUM(fp8rt_act) { FP8RT_SILU = 0, FP8RT_GELU = 1 } fp8rt_act;
  *   order   : int32 [tokens * k]; slot s holds choice order[s] = t k + j; entries from
  *             offsets[experts] on are left as they were
  *   slots   : slots[t,j], the slot of that choice
- * experts <= 1024, k <= 32, groups <= 64 (else FP8RT_EUNSUPPORTED); groups divides experts; k <= experts / groups *
+ * experts <= 1024, k <= 32, groups <= 64, tokens <= 2^27 (else FP8RT_EUNSUPPORTED); groups divides experts; k <= experts / groups *
  * top_groups; tokens * k < 2^31; scale finite.  Alignment: pointers to their element.
  * Scratch: the per-stream scratch buffer holds up to experts bytes for each 8 tokens. */
 fp8rt_status fp8_expert_route(const void* logits, fp8rt_dtype lt, int64_t tokens, int64_t experts, int64_t ld,

@@ -42,6 +42,7 @@ ROUTE_BAD = [
     (dict(slots=None, order=None), "EINVAL"), (dict(groups=0), "EINVAL"), (dict(top=0), "EINVAL"),
     (dict(top=5), "EINVAL"), (dict(best=0), "EINVAL"), (dict(best=3), "EINVAL"), (dict(groups=5, top=5), "EINVAL"),
     (dict(k=17, top=1), "EINVAL"), (dict(experts=130, ld=130, groups=65), "EUNSUPPORTED"),
+    (dict(tokens=2 ** 27 + 1, k=1), "EUNSUPPORTED"),
     (dict(w=FAKE + 1), "EALIGN"), (dict(bias=FAKE + 2), "EALIGN"), (dict(slots=FAKE + 2), "EALIGN"),
     (dict(order=FAKE + 3), "EALIGN"), (dict(offsets=FAKE + 1), "EALIGN"),
 ])
