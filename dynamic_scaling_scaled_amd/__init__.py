@@ -574,7 +574,8 @@ def _live(t):
 def fp8_expert_route(logits, ids, weights, slots=None, order=None, offsets=None, score=SOFTMAX, bias=None, groups=1,
                      top_groups=1, group_best=1, renormalise=True, scale=1.0, stream=None):
     """The k experts of each token (ids, weights: [tokens x k]) from the router's logits [tokens x experts], and
-    the plan that sorts the choices by expert: slots [tokens x k], order [tokens k], offsets [experts + 1]."""
+    the plan that sorts the choices by expert: slots [tokens x k], order [tokens k], offsets [experts + 1].
+    A bias of -inf or nan switches its expert off."""
     tokens, experts, ld = _mat(logits)
     shape = ids.shape
     if len(shape) != 2 or shape[0] != tokens:

@@ -125,7 +125,9 @@ __device__ __forceinline__ void load_logits(const T* row, int lane, int E, float
 #pragma unroll
   for (int v = 0; v < NV; ++v) l[v] = lane * NV + v < E ? logit(wide(raw[v])) : -INFINITY;
 }
-// The same of the bias: 0 without one.
+// The same of the bias: 0 without one.  -Inf and NaN switch an expert off: its key would be -Inf or NaN, neither of which
+// orders against an empty place.
+__device__ __forceinline__ bool chosen_from(float l, float bias) { return l > -INFINITY && bias > -INFINITY; }
 template <int NV>
 __device__ __forceinline__ void load_bias(const float* bias, int lane, int E, float (&b)[NV]) {
 #pragma unroll
@@ -284,7 +286,7 @@ __device__ __forceinline__ void choose_exactly(const RouteArgs& a, const Groups&
   if (a.score == FP8RT_SOFTMAX) sum = run_sum<L>(sum);
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    const bool there = l[v] > -INFINITY;
+    const bool there = chosen_from(l[v], bias[v]);
     if (a.score == FP8RT_SOFTMAX) p[v] /= sum;
     p[v] += static_cast<double>(bias[v]);
     group[v] = there ? rising(p[v]) : 0;
@@ -333,7 +335,7 @@ __device__ __forceinline__ void order_exactly(const RouteArgs& a, const T* row, 
     sum = run_sum<L>(sum);
   }
   const int id = near && lane <= a.k ? out[lane] : -1;
-  double key = -INFINITY;
+  double key = -INFINITY;  // of an empty place: behind every expert's, whose bias is above it
   if (id >= 0) {
     const double l = load_logit(row + id);
     key = (a.score == FP8RT_SOFTMAX ? exp(l - static_cast<double>(m)) / sum : 1.0 / (1.0 + exp(-l))) +
@@ -374,7 +376,7 @@ __device__ __forceinline__ Settled choose(const RouteArgs& a, const Groups& gr, 
         p[v] = fast_exp(l[v] - m) * inv;
       else
         p[v] = __builtin_amdgcn_rcpf(1.0f + fast_exp(-l[v]));
-      const bool there = l[v] > -INFINITY;
+      const bool there = chosen_from(l[v], bias[v]);
       p[v] += bias[v];
       group[v] = there ? rising32(p[v]) : 0;
       key[v] = a.bias ? group[v] : there ? rising32(l[v]) : 0;

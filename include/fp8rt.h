@@ -587,6 +587,8 @@ typedef FP8RT_ENUM(fp8rt_act) { FP8RT_SILU = 0, FP8RT_GELU = 1 } fp8rt_act;
  *   an expert whose logit is -Inf or NaN is absent: p = 0, and it is never chosen (+Inf counts as the
  *   largest finite value)
  *   key[e] = p[e] + bias[e], or without a bias the logit itself
+ *   an expert whose bias is -Inf or NaN is switched off: it is never chosen and counts in no run's score (its logit
+ *     still counts in a softmax's sum); +Inf comes before every finite key
  *   groups > 1: the experts form `groups` runs of experts / groups; a run's score is its largest key
  *     (group_best 1) or the sum of its two largest p[e] (+ bias[e]) (group_best 2; the one alone if
  *     it has no second); the top_groups best runs stay (ties to the lower run)

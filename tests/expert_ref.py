@@ -13,7 +13,8 @@ HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}  # half a step, re
 
 
 def route(logits, k, score="softmax", bias=None, groups=1, top=1, best=1, renorm=True, scale=1.0):
-    """(ids [tokens][k], weights [tokens][k], bound of the weights' relative error) token after token."""
+    """(ids [tokens][k], weights [tokens][k], bound of the weights' relative error) token after token.  A bias of -Inf or
+    NaN switches its expert off for the choice."""
     ids, weights, bounds = [], [], []
     for row in logits.double().tolist():
         E = len(row)
@@ -28,6 +29,7 @@ def route(logits, k, score="softmax", bias=None, groups=1, top=1, best=1, renorm
             p = [(1 / (1 + math.exp(-x)) if x > -700 else math.exp(x)) if t else 0.0 for x, t in zip(l, there)]
         with_bias = p if bias is None else [x + b for x, b in zip(p, bias.double().tolist())]
         key = l if bias is None else with_bias
+        there = [t and x > -math.inf for t, x in zip(there, key)]  # (False for NaN)
         open_ = set(range(E))
         if groups > 1:
             n, found = E // groups, []
