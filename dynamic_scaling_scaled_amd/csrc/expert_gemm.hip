@@ -375,12 +375,14 @@ __device__ __forceinline__ void tile_body(const ExpertGemmArgs& g, TileShared<BL
       sb[j][e] = g.sb[t.expert * g.sb_expert + min(col0 + 16 * j + 4 * q + e, g.N - 1) * g.sb_col];
   constexpr int kRowBytes = 64 * sizeof(O), kChunks = kRowBytes / 16;
   constexpr int kSlot = TileShared<BLOCKS>::kSlot;
-  constexpr int kRows = 64 * NB < kSlot / kRowBytes ? 64 * NB : kSlot / kRowBytes;  // rows of one pass
+  constexpr int kRows = 64 * NB < kSlot / kRowBytes ? 64 * NB : kSlot / kRowBytes;  // rows of one pass, the last may have fewer
+  static_assert(kRows % 16 == 0, "whole row tiles");
   uint8_t* mine = sh.ring + p.wave * kSlot;
 #pragma unroll
   for (int r0 = 0; r0 < 64 * NB; r0 += kRows) {
+    const int rows = 64 * NB - r0 < kRows ? 64 * NB - r0 : kRows;  // (192 fp32 rows: 128 and 64)
 #pragma unroll
-    for (int i = r0 / 16; i < (r0 + kRows) / 16; ++i) {
+    for (int i = r0 / 16; i < (r0 + rows) / 16; ++i) {
       const int r = 16 * i + fr;
       const float sa = sh.scale[r];
       const bool none = sh.row[r] < 0;
@@ -394,7 +396,7 @@ __device__ __forceinline__ void tile_body(const ExpertGemmArgs& g, TileShared<BL
         store4(reinterpret_cast<O*>(dst), v);
       }
     }
-    for (int c = p.lane; c < kRows * kChunks; c += 64) {
+    for (int c = p.lane; c < rows * kChunks; c += 64) {
       const int r = c / kChunks, k = c % kChunks;
       const int64_t s = t.row0 + r0 + r, col = col0 + k * (16 / static_cast<int>(sizeof(O)));
       const u32x4 v = *reinterpret_cast<const u32x4*>(mine + r * kRowBytes + ((k ^ (r & 7)) << 4));
