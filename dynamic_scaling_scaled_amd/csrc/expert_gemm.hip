@@ -405,16 +405,6 @@ __device__ __forceinline__ void tile_body(const ExpertGemmArgs& g, TileShared<BL
   }
 }
 
-// Joins the workgroup's barrier with the wave's LDS operations done; loads keep flying.
-__device__ __forceinline__ void lds_join() {
-  __builtin_amdgcn_sched_barrier(0);
-  __atomic_signal_fence(__ATOMIC_SEQ_CST);
-  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
-  __builtin_amdgcn_s_barrier();
-  __atomic_signal_fence(__ATOMIC_SEQ_CST);
-  __builtin_amdgcn_sched_barrier(0);
-}
-
 // Tiles of up to BLOCKS blocks of 64 slots.  Four blocks take most of the registers and the LDS (one workgroup a CU); with
 // one block a second workgroup fills the first one's start, end and barriers.
 template <int FA, typename O, int BLOCKS>
@@ -446,7 +436,7 @@ __global__ void __launch_bounds__(kTileThreads, BLOCKS == 4 ? 1 : 2) k_expert_ti
     sh.row[tid] = static_cast<int>(row);
     sh.scale[tid] = g.sa[g.sa_rows ? max(row, int64_t(0)) : 0];
   }
-  lds_join();
+  lds_barrier();
   const int nb = static_cast<int>((min(t.end - t.row0, int64_t(TM)) + 63) / 64);
 #pragma unroll
   for (int j = 0; j < 2 * BLOCKS; ++j) {

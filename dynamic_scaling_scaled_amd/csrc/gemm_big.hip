@@ -288,17 +288,6 @@ __device__ __forceinline__ void acc_fence(f32x4 (&acc)[MI16][NJ16]) {
                  "+a"(acc[7][4]), "+a"(acc[7][5]), "+a"(acc[7][6]), "+a"(acc[7][7]));
 }
 
-// Wait for this wave's LDS reads (its vector-memory loads keep flying) and
-// join the workgroup barrier.
-__device__ __forceinline__ void lds_barrier() {
-  __builtin_amdgcn_sched_barrier(0);
-  __atomic_signal_fence(__ATOMIC_SEQ_CST);
-  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0), vmcnt and expcnt at their maximum
-  __builtin_amdgcn_s_barrier();
-  __atomic_signal_fence(__ATOMIC_SEQ_CST);
-  __builtin_amdgcn_sched_barrier(0);
-}
-
 // One MFMA of row tile I, column tile J: plain, or with the exponent bytes
 // I % 4 of xa and J % 4 of xb (1x32 scales).
 template <int FA, bool MX>

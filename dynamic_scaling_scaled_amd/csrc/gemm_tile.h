@@ -1,5 +1,5 @@
 // gemm_tile.h -- pieces that the large GEMM and the experts' GEMM share: operand types,
-// buffer-to-LDS loads, the barrier between stages and the 16x16x128 MFMA.
+// buffer-to-LDS loads, the barriers and the 16x16x128 MFMA.
 #pragma once
 
 #include "device_common.h"
@@ -31,6 +31,17 @@ __device__ __forceinline__ void step_barrier() {
   __builtin_amdgcn_sched_barrier(0);
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
   __builtin_amdgcn_s_waitcnt(((N >> 4) << 14) | 0x0070 | (N & 15));
+  __builtin_amdgcn_s_barrier();
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// Wait for this wave's LDS operations (its vector-memory loads keep flying) and
+// join the workgroup barrier.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_sched_barrier(0);
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0), vmcnt and expcnt at their maximum
   __builtin_amdgcn_s_barrier();
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
   __builtin_amdgcn_sched_barrier(0);
