@@ -634,8 +634,8 @@ fp8rt_status fp8_expert_route_backward(const void* logits, fp8rt_dtype lt, int64
  *   slots : rows of y (and entries of order), a bound on offsets[experts]
  *   y  : [slots x N] bf16 / fp32 (ldy); rows of no expert are left as they were
  * The device's integers are not trusted: offsets are clamped to [0, slots], an expert whose end lies before its
- * start has no slots, and where experts claim the same slots it is open which of the claims are served; a slot
- * whose r lies outside [0, a_rows) is 0.
+ * start has no slots; where experts claim the same slots it is open which of the claims are served, and where they claim
+ * more than there are slots, some slots may be left as they were; a slot whose r lies outside [0, a_rows) is 0.
  * Format pairs: E4M3 x E4M3 and E5M2 x E4M3 (a data gradient: the same call with the K-major weights).
  * Granularities: ga row {1,0} or tensor {0,0}; gb channel {1,0}, expert {N,0} or tensor {0,0}; else
  * FP8RT_EUNSUPPORTED.  flags: FP8RT_B_PACKED16, which is required (without it FP8RT_EUNSUPPORTED: decode and
