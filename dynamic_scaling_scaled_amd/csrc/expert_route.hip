@@ -502,7 +502,8 @@ __global__ void __launch_bounds__(NV <= 4 ? 2 * kThreads : kThreads) k_route(Rou
       const float total = run_sum<L>(there ? q : 0.0f);
       w = q / total;
     } else if (a.score == FP8RT_SIGMOID) {
-      w = 1.0f / (1.0f + expf(-cl));
+      const float c = expf(-fabsf(cl));  // (e^-cl itself would overflow where the weight is still a number)
+      w = (cl > 0.0f ? 1.0f : c) / (1.0f + c);
     } else {
       w = expf(cl - m) / sum;
     }
