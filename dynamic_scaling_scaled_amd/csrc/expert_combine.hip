@@ -4,7 +4,9 @@
 //   y[t] = residual[t] + sum_j w[t,j] x[slot(t,j)];   dx[slot(t,j)] = w[t,j] dy[t],   dw[t,j] = <dy[t], x[slot(t,j)]>
 //
 // Bound by memory: every row once (4096 tokens of 8 x 7168 bf16: 587 MB forward, 998 back).  Measured: 126 us (4.7 TB/s)
-// and 201 us (5.0 TB/s; a large copy reaches 4.8); a step of 64 tokens 4.9 us, of which a launch is 3.
+// and 201 us (5.0 TB/s; a large copy reaches 4.8); a step of 64 tokens 4.9 us, of which a launch is 3.  1365 tokens of 24
+// experts, bf16: 115 and 276 us (4.4 and 3.5 TB/s: 32 partial products a thread leave fewer waves); fp32, 1024 of 16 117 and 203
+// (4.5 and 4.8), 512 of 32 114 and 217 (4.4 and 4.4, 12 registers spilled).
 #include <algorithm>
 
 #include "device_common.h"

@@ -3,9 +3,10 @@
 //
 //   y[s,n] = s_a(r) s_b(e,n) sum_k dec(a[r,k]) dec(b[e,n,k]),   offsets[e] <= s < offsets[e+1]
 //
-// Bounds: the weights of the experts that are used, read once (6.1 TB/s), against 2 slots N K operations (this library's
-// large GEMM reaches 2.3 PFLOP/s).  Measured, 4096 x 7168 (N x K): one token of 8 experts 36.7 us (6.4 TB/s), a step of 64
-// tokens, 8 of 128 experts, 498 us (6.3 TB/s), 1024 slots for each of 32 experts 780 us (2.46 PFLOP/s); 7168 x 2048,
+// Bounds: the weights of the experts that are used, read once (8 TB/s at most; a read-only pass over 4 GiB reaches 6.1), against
+// 2 slots N K operations (5 PFLOP/s at most; the library product of 8192^3 reaches 3.15 and this library's large GEMM 2.3).
+// Measured, 4096 x 7168 (N x K): one token of 8 experts 36.7 us (6.4 TB/s), a step of 64
+// tokens, 8 of 128 experts, 498 us (6.3 TB/s), 1024 slots for each of 32 experts 775 to 810 us (2.38 to 2.48 PFLOP/s); 7168 x 2048,
 // 2804 slots very unequally over 32 experts 106 us (4.2 TB/s: the few experts with hundreds of slots are bound by
 // the matrix cores while the others' weights arrive, and a workgroup has 16 stages only).
 #include <algorithm>
@@ -100,7 +101,9 @@ __device__ __forceinline__ bool find_unit(const ExpertGemmArgs& g, int b, int co
       const int at = __ffsll(static_cast<unsigned long long>(past)) - 1;
       const int rows = __builtin_amdgcn_readlane(n, at);
       index -= __builtin_amdgcn_readlane(s, at) - rows * col_tiles;
-      if (index < 0 || index >= rows * col_tiles) return false;  // (sums of claims on the same slots may wrap)
+      // (Never so: of 1024 experts at most 512 can claim all slots, whose units stay below 2^31 by the host's bound on tiles.  A
+      // unit outside its expert would be written outside y.)
+      if (index < 0 || index >= rows * col_tiles) return false;
       const int first = index / (4 * col_tiles) * 4, in = index - first * col_tiles, m = min(4, rows - first);
       t.expert = e0 + at;
       t.row0 = __builtin_amdgcn_readlane(lo, at) + static_cast<int64_t>(first + in % m) * TM;
@@ -465,17 +468,21 @@ __global__ void __launch_bounds__(kTileThreads, BLOCKS == 4 ? 1 : 2) k_expert_ti
 
 // Which kernel.  The host knows the slots and the experts, not how the plan shares them out, so the rule goes by the
 // average a = slots / experts and by the units that the tile kernel would have at least.  Measured, experts x slots of each,
-// us (the weights alone at 6.1 TB/s in brackets):
+// us (in brackets the weights alone at the 6.1 TB/s of a read-only pass):
 //   stream of 16 slots / of 32, tiles of 64 / of 256
 //     4096 x 7168:  32 x 4 139 / 144, 159 / 160 (154);  32 x 16 169 / 153, 161 / 163;  8 x 16 44 / 44, 52 / 53 (38);
 //                   8 x 32 67 / 54, 54 / 55;  2 x 16 14 / 16, 27 / 27 (10);  2 x 32 25 / 17, 27 / 27
-//     7168 x 2048:  32 x 8 88 / 98, 88 / 92 (77);  32 x 32 170 / 110, 92 / 98
+//                   32 x 8 142 / 144, 159 / 161;  of 32 with 8 on average, one has 64: 166 / 195, 159 / 161, one has 200: 184 / 196,
+//                   182 / 171;  with 16, one has 300: 239 / 200, 184 / 210;  with 32, one has 700: 347 / 258, 183 / 203
+//     7168 x 2048:  32 x 8 88 / 98, 88 / 92 (77), one has 200: 100 / 108, 86 / 95;  32 x 32 170 / 110, 92 / 98, one has 700:
+//                   176 / 138, 99 / 111
 //   tiles of 64 / of 256
 //     4096 x 7168:  32 x 64 169 / 171, 32 x 128 213 / 190;  8 x 64 58 / 59, 8 x 128 59 / 67, 8 x 160 84 / 73
 //     4096 x 4096:  32 x 88 121 / 107, of 32 with 96 on average but unequal 131 / 139;  8 x 88 30 / 37
 //     7168 x 2048:  32 x 88 112 / 116, of 88 on average but unequal 124 / 142;  32 x 128 118 / 121, 32 x 256 182 / 154
 //     4096 x 1024:  32 x 128 43 / 48, 32 x 192 59 / 58, of 178 on average but unequal 58 / 68
-// A few slots an expert are streamed, up to 32 where tiles would not fill the CUs.  Tiles of 256 read the weights
+// A few slots an expert are streamed, up to 32 where tiles would not fill the CUs (also where one expert has most of them: up to
+// 17% slower than tiles of 64 at an average of 8, which the host cannot see).  Tiles of 256 read the weights
 // from the L2 cache a quarter as often; those of 64, two workgroups a CU, waste less of a CU on starts, ends, partial tiles and
 // uneven shares.  So the latter take up to 64 slots, more the shorter their loops (a K up to 2^18) and up to 128 where all of
 // them run at once.

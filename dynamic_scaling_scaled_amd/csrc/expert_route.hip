@@ -10,10 +10,13 @@
 // a 64-bit mask; a choice's place among its expert's is the number of set bits below its token (stable and free of
 // atomics on counters), and a workgroup's count is the mask's population.
 //
-// Measured (kernels alone): a token of 64 experts 4.6 us, of which a launch is 3; 4096 tokens of 64 (k 6, bf16) 7.3 us, their
-// plan 4.7, the gradient 4.9; 8192 of 256 (k 8 of 4 of 8 groups, biased sigmoids) 18 us and the plan 5.9.  The bytes
-// (8 MiB of logits there) would take 2 us: what bounds it is the chain of k + 2 rounds of a maximum over the token's lanes, of 10
-// to 14 dependent instructions each, hidden by the other waves of a SIMD.  Bounds of 8 waves a SIMD spill (30 us).
+// Measured (kernels alone): a token of 64 experts 4.6 us, of which a launch is 3; 16384 tokens of 64 (k 6, bf16) 7.5 us, their
+// plan 4.2, the gradient 4.7; 8192 of 256 (k 8 of 4 of 8 groups, biased sigmoids) 19 us and the plan 5.8, of 512 35 and 9.  The
+// bytes (8 MiB of logits there) would take 2 us: what bounds it is the chain of k + 2 rounds of a maximum over the token's lanes, of
+// 10 to 14 dependent instructions each, hidden by the other waves of a SIMD.  The 64-bit path lives in the same kernel: it sets
+// the registers (101 up to 4 experts a lane, so 4 waves a SIMD; bounds of 8 waves spill, 30 us) and 19 to 63 scalar ones are kept in
+// vector lanes.  Past 512 experts (16 a lane) its arrays spill 159 vector registers: 8192 tokens of 1024 take 111 us with groups and
+// bias and 72 with plain softmax (of 600 69), the plan 15.
 #include <float.h>
 
 #include <algorithm>
@@ -709,7 +712,8 @@ hipError_t launch_expert_route(const RouteArgs& a, hipStream_t st) {
     constexpr int L = decltype(l)::value, NV = decltype(nv)::value;
     // One workgroup finishes the plan by itself where its runs take at most two rounds (the plan's launch costs about as
     // much as a round).  Else about 256 workgroups, each of at least a round of kThreads (4096 tokens of 16 lanes in
-    // 256 blocks of 16: 9.9 us and their plan 9.2, in 128 of 32: 7.6 and 6.4) and of at most a mask's 64 tokens.
+    // 256 blocks of 16: 9.9 us and their plan 9.2, in 128 of 32: 7.6 and 6.4; both together in 128 of 32 9.3, in 64 of 64 10.1) and
+    // of at most a mask's 64 tokens (16384 in 256 blocks of 64: 10.7 us with the plan, in 512 of 32 12.4).
     constexpr int kRuns = kThreads / L;
     if (a.tokens <= 2 * kRuns)
       plan.tokens = 2 * kRuns;

@@ -7,7 +7,9 @@
 // Bound by memory: bf16 reads 4 bytes and writes 1 for each of z's values, 2 more with the checkpoint; the gradient
 // reads 4 and writes 4, 2 more with z.  Measured: 4096 rows of 29568 columns, one scale a row, 106 us (5.7 TB/s); 8189 of
 // 7168 in groups of 128 with the checkpoint 92 us (4.5 TB/s: three exact scales and three casts for each 128 columns
-// keep the vector units as busy as the memory) and the gradient with z 98 (6.0 TB/s).
+// keep the vector units as busy as the memory) and the gradient with z 98 (6.0 TB/s).  One scale a row beside the checkpoint:
+// 4096 of 16384 columns 82 to 95 us (4.9 to 5.7 TB/s), of 29568 209 (4.1), 2048 of 65536 377 (2.5: see k_gated_rows); fp32 rows
+// without it 230 (4.7) and 291 (4.2), with it 286 for 29568 (4.7), and its gradient 460 (4.7).
 #include <algorithm>
 #include <type_traits>
 
@@ -23,8 +25,9 @@ constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kGeluA = 1.5957691216057307f;  // 2 sqrt(2 / pi)
 constexpr float kGeluB = 0.044715f;
 
-// c of a gate: 1 / (1 + 2^(-v log2 e)).  The hardware's exponential and reciprocal (1 ulp each); an
-// overflowing exponential gives c = 0.
+// c of a gate: 1 / (1 + 2^(-v log2 e)).  The product is rounded before the exponential, which costs |v| u, v itself is
+// rounded in up to 4 operations, and the hardware's exponential and reciprocal are off by 1 ulp each: (6 |v| + 16) u in all, for
+// values that are next rounded to 8 bits or by a gradient's casts.  The reciprocal gives 0 for a c below 2^-126 (v below -87.3).
 template <int ACT>
 __device__ __forceinline__ float gate_c(float g) {
   float v = g;
@@ -226,7 +229,8 @@ __global__ void __launch_bounds__(256) k_gated_groups(GatedArgs a, int rows_per,
 
 // One scale a row: z stays in registers between the row's maximum and its cast, with the next row's loads in flight.  A row
 // is L lanes of a wave (a power of two), or the whole workgroup (L = 0); a thread holds octets t, t + threads, ... (NV of
-// them).
+// them).  1024 threads leave 128 registers each.  What is left over goes to scratch memory: 18 of them for bf16 rows of 4 octets
+// with a checkpoint (past 16384 columns), 79 to 93 for 8 octets with one (past 32768), 34 for fp32 rows of 8 octets without.
 template <typename T, int F, int ACT, int NV, bool KEPT>
 __global__ void __launch_bounds__(1024) k_gated_rows(GatedArgs a, int lanes_per_row, int64_t rows_at_once) {
   __shared__ uint32_t sh[2][kMaxWaves];
@@ -239,7 +243,7 @@ __global__ void __launch_bounds__(1024) k_gated_rows(GatedArgs a, int lanes_per_
   if (live == 0) return;
   const int64_t row0 = L ? (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) / L : blockIdx.x;
   const int lanes = L && L < kKeptRun ? L : kKeptRun;
-  constexpr bool kHold = NV * sizeof(T) <= 8;  // (fp32 rows and 8 octets would spill)
+  constexpr bool kHold = NV * sizeof(T) <= 8;  // (more loads in flight than that would only be spilled)
   Octet<T> go[NV], uo[NV];
   auto load = [&](int64_t row) {  // (rows past the end load the last one again)
     const T* gp = x + (row < live ? row : live - 1) * a.ldx;

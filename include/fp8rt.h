@@ -595,7 +595,7 @@ typedef FP8RT_ENUM(fp8rt_act) { FP8RT_SILU = 0, FP8RT_GELU = 1 } fp8rt_act;
  *   ids[t,:]     the k largest keys of the runs that stay, in falling order, ties to the lower expert
  *   weights[t,j] = scale p[ids[t,j]], divided by the sum of the chosen p if renormalise
  * Keys with a bias and sums of two are formed and compared in binary64 (a binary32 score would choose
- * differently at a border); weights are binary32.  A place that finds no expert (fewer than k
+ * differently at a border); weights are formed in binary32.  A place that finds no expert (fewer than k
  * present) has id -1, weight 0 and slot -1.
  *   logits : [tokens x experts] fp32 / bf16 (lt), leading dimension ld;  bias : nullable [experts] fp32
  *   ids, weights, slots : [tokens][k] int32, fp32, int32
@@ -626,7 +626,8 @@ fp8rt_status fp8_expert_route_backward(const void* logits, fp8rt_dtype lt, int64
 
 /* The experts' scaled products: slot s, of the expert e with offsets[e] <= s < offsets[e+1], is
  *   y[s,n] = s_a(r) s_b(e,n) sum_k dec(a[r,k]) dec(b[e,n,k]),   r = order[s] / choices, or s if order is NULL
- * with the FP8 matrix cores' products and FP32 accumulation of fp8_scaled_gemm.
+ * with the FP8 matrix cores' products (a run of 8 loses less than 7 * 2^-13 of its largest |product|) and FP32
+ * accumulation of fp8_scaled_gemm.  The exact products that fp8_scaled_gemm has for small weights are not offered here.
  *   a  : [a_rows x K] codes (lda), format fa, scales scale_a with granularity ga
  *   b  : the experts' weights [experts N x K] as one fp8_pack_weights16 image (fp8_quantize_packed16
  *        writes it), format fb; scales scale_b with granularity gb of that matrix
@@ -651,7 +652,8 @@ fp8rt_status fp8_expert_gemm(const uint8_t* a, fp8rt_format fa, int64_t a_rows, 
 
 /* Gated activation with an FP8 output: the operand of the down projection in one pass
  * over the output of the gate and up projection.
- *   z[i,j] = act(x[i,j]) x[i,cols+j]             (binary32)
+ *   z[i,j] = act(x[i,j]) x[i,cols+j]             (binary32, relative error up to (6 |v| + 16) 2^-24 with v as in
+ *                                                 fp8rt_act, v = g for SiLU; 1 / (1 + e^-v) below 2^-126 counts as 0)
  *   q, scale, inv_scale = fp8_quantize(z, g, f, mode, eps, pow2_round_up)
  *   x    : [rows x 2 cols] fp32 / bf16 (ldx): the gates, then the ups
  *   kept, kept_scale : nullable (both or neither): x as an 8-bit checkpoint for fp8_gated_backward, each half
@@ -673,7 +675,7 @@ fp8rt_status fp8_gated_quantize(const void* x, fp8rt_dtype xt, int64_t rows, int
 
 /* Gradient of z = act(g) u from the checkpoint (the casts count as the identity).  With g, u the
  * values that kept's codes stand for (fl32(scale dec(code))):
- *   dx[i,j] = dz[i,j] u act'(g),  dx[i,cols+j] = dz[i,j] act(g),  z[i,j] = act(g) u
+ *   dx[i,j] = dz[i,j] u act'(g),  dx[i,cols+j] = dz[i,j] act(g),  z[i,j] = act(g) u     (precision as above)
  *   dz : [rows x cols] fp32 / bf16 (t, lddz);  dx : [rows x 2 cols] of type t (lddx)
  *   z  : nullable [rows x cols] of type t (ldz): the activation computed again, for the down projection's weight
  *        gradient
