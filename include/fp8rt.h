@@ -596,7 +596,7 @@ typedef FP8RT_ENUM(fp8rt_act) { FP8RT_SILU = 0, FP8RT_GELU = 1 } fp8rt_act;
  *   weights[t,j] = scale p[ids[t,j]], divided by the sum of the chosen p if renormalise
  * Keys with a bias and sums of two are formed and compared in binary64 (a binary32 score would choose
  * differently at a border); weights are formed in binary32.  A place that finds no expert (fewer than k
- * present) has id -1, weight 0 and slot -1.
+ * to choose from) has id -1, weight 0 and slot -1.
  *   logits : [tokens x experts] fp32 / bf16 (lt), leading dimension ld;  bias : nullable [experts] fp32
  *   ids, weights, slots : [tokens][k] int32, fp32, int32
  * The plan (slots, order, offsets: all three, or all NULL): the choices in the order of expert, then token.
