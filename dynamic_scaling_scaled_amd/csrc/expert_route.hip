@@ -128,9 +128,10 @@ __device__ __forceinline__ void load_logits(const T* row, int lane, int E, float
 #pragma unroll
   for (int v = 0; v < NV; ++v) l[v] = lane * NV + v < E ? logit(wide(raw[v])) : -INFINITY;
 }
-// The same of the bias: 0 without one.  -Inf and NaN switch an expert off: its key would be -Inf or NaN, neither of which
+// Whether an expert may be chosen.  A bias of -Inf or NaN switches it off: its key would be one of these, neither of which
 // orders against an empty place.
 __device__ __forceinline__ bool chosen_from(float l, float bias) { return l > -INFINITY && bias > -INFINITY; }
+// The same of the bias as of the logits: 0 without one.
 template <int NV>
 __device__ __forceinline__ void load_bias(const float* bias, int lane, int E, float (&b)[NV]) {
 #pragma unroll

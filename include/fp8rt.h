@@ -675,7 +675,7 @@ fp8rt_status fp8_gated_quantize(const void* x, fp8rt_dtype xt, int64_t rows, int
 
 /* Gradient of z = act(g) u from the checkpoint (the casts count as the identity).  With g, u the
  * values that kept's codes stand for (fl32(scale dec(code))):
- *   dx[i,j] = dz[i,j] u act'(g),  dx[i,cols+j] = dz[i,j] act(g),  z[i,j] = act(g) u     (precision as above)
+ *   dx[i,j] = dz[i,j] u act'(g),  dx[i,cols+j] = dz[i,j] act(g),  z[i,j] = act(g) u   (terms as precise as above)
  *   dz : [rows x cols] fp32 / bf16 (t, lddz);  dx : [rows x 2 cols] of type t (lddx)
  *   z  : nullable [rows x cols] of type t (ldz): the activation computed again, for the down projection's weight
  *        gradient
